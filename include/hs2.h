@@ -288,6 +288,130 @@ hs2_status hs2_decode_stage(const hs2_decode_shape* shape, const void* k_cache,
 hs2_status hs2_decode_sparse_staged(const hs2_decode_shape* shape, const void* q,
                                     const void* staged, void* o, hs2_stream_t stream);
 
+/*
+ * ------------------------------------------------ caches held in 8 bits
+ *
+ * Two cache formats, both with separate K and V storage of e4m3 codes:
+ *   token cache   codes [B, Tmax, d], scales [B, Tmax] fp32: the cache that
+ *                 hs2_decode_select and hs2_decode_sparse read (one KV head);
+ *   paged cache   a pool of pages [n_pages, Hkv, page, d] with one fp32 scale
+ *                 per page and KV head, [n_pages, Hkv], and for each sequence
+ *                 a row of page numbers, table [B, max_pages] int32: position
+ *                 s of sequence b is row s % page of page table[b, s / page].
+ * A stored value is scale * e4m3(code).  e4m3(x) rounds to nearest, ties to
+ * even, and saturates at +-448.
+ *
+ * Rows that a call writes or reads: `start` [B] int32 (device) gives each
+ * sequence's first cache position, `count` [B] int32 (device, may be NULL: N
+ * each) how many of the N rows of k_new / v_new / k / v it uses, from row 0;
+ * zero is allowed.  Rows past the count are neither read nor written.  A
+ * sequence whose start or count is out of range (count outside [0, N], start
+ * outside [0, capacity - count]) is left alone, as is a page number outside
+ * [0, n_pages); both raise HS2_ERR_DEVICE_DATA as above.
+ */
+typedef struct {
+    int B, Tmax, d;  /* sequences, cache rows per sequence, head dim (64 or 128) */
+} hs2_cache_shape;
+
+typedef struct {
+    int B, Hkv, d;   /* sequences, KV heads, head dim (64 or 128) */
+    int page;        /* tokens per page: 16, 32, 64 or 128 */
+    int n_pages;     /* pages in the pool */
+    int max_pages;   /* entries in a sequence's table row */
+} hs2_paged_shape;
+
+/*
+ * Quantise K/V rows as they are written to the token cache.
+ *   k_new, v_new [B, N, d] bf16
+ *   k_cache, v_cache [B, Tmax, d] e4m3 codes, k_scale, v_scale [B, Tmax] fp32:
+ *       in/out; rows start[b] .. start[b] + count[b] - 1 are written
+ * scale = max|x| / 448 of the row, 1 for a row of zeros, and code = e4m3(x /
+ * scale), both in fp32.  Infinities and NaN in a row are left out of its
+ * maximum, stored as +-448 scale and NaN, and flagged (HS2_ERR_DEVICE_DATA).
+ */
+hs2_status hs2_kv_write(const hs2_cache_shape* shape, int N, const void* k_new, const void* v_new,
+                        const int32_t* start, const int32_t* count, void* k_cache, void* v_cache,
+                        float* k_scale, float* v_scale, hs2_stream_t stream);
+
+/*
+ * Read rows of the token cache back: k, v [B, N, d] bf16 out, row i of
+ * sequence b = bf16(scale * e4m3(code)) of cache row start[b] + i, for
+ * i < count[b]; e.g. the cached part of a prompt whose next chunk is to attend
+ * to it through hs2_full_attn_rows or hs2_window_attn.
+ */
+hs2_status hs2_kv_read(const hs2_cache_shape* shape, int N, const void* k_cache, const void* v_cache,
+                       const float* k_scale, const float* v_scale, const int32_t* start,
+                       const int32_t* count, void* k, void* v, hs2_stream_t stream);
+
+/*
+ * Quantise K/V rows as they are written to the paged cache.
+ *   k_new, v_new [B, N, Hkv, d] bf16
+ *   k_pages, v_pages [n_pages, Hkv, page, d] e4m3 codes, k_scale, v_scale
+ *       [n_pages, Hkv] fp32: in/out
+ * For each page and head that rows of the call fall into, p = the least power
+ * of two >= 2^-126 with max|x| <= 448 p over those rows.  A page whose first
+ * row the call writes gets scale p.  A page that holds earlier rows keeps its
+ * scale s if s >= p; otherwise its scale becomes p and the earlier rows' codes
+ * become e4m3(code * s / p).  Then code = e4m3(x / scale).  A page's rows
+ * behind the last one written hold nothing: a later call may write them.  The
+ * pages that one call writes must be distinct (a page shared by sequences is
+ * for reading).  Infinities and NaN as in hs2_kv_write; an earlier scale that
+ * is not finite and positive is flagged and replaced by p.
+ */
+hs2_status hs2_paged_kv_write(const hs2_paged_shape* shape, int N, const void* k_new,
+                              const void* v_new, const int32_t* table, const int32_t* start,
+                              const int32_t* count, void* k_pages, void* v_pages, float* k_scale,
+                              float* v_scale, hs2_stream_t stream);
+
+/* Read rows of the paged cache back: k, v [B, N, Hkv, d] bf16 out (hs2_kv_read). */
+hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_pages,
+                             const void* v_pages, const float* k_scale, const float* v_scale,
+                             const int32_t* table, const int32_t* start, const int32_t* count,
+                             void* k, void* v, hs2_stream_t stream);
+
+/*
+ * Decode attention over the paged cache: one query token per sequence, at
+ * position lengths[b] - 1, over the positions s < lengths[b] that lie in the
+ * last `window` of them or among the first `n_sink` (window = INT_MAX: all).
+ *   Hq       query heads, a multiple of Hkv, at most 16 per KV head; query
+ *            head h reads KV head h / (Hq / Hkv)
+ *   q        [B, Hq, d] bf16, finite
+ *   k_pages, v_pages, k_scale, v_scale: any scales that are finite and > 0
+ *   lengths  [B] int32, device, each in [0, max_pages * page]; a length of 0
+ *            gives o = 0 and lse = -inf, one out of range the same and a flag
+ *   o        [B, Hq, d] bf16 out;  lse [B, Hq] fp32 out (natural log), may be NULL
+ *   workspace: >= hs2_paged_decode_workspace() bytes (0 for an invalid shape),
+ *   no initialisation needed; calls on the same workspace must not overlap.
+ * Positions on a page number outside [0, n_pages) are left out and flagged.
+ * Rows of a page behind the sequence's last token are never used, whatever
+ * they hold.
+ */
+size_t hs2_paged_decode_workspace(const hs2_paged_shape* shape, int Hq);
+hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, int n_sink,
+                            float scale, const void* q, const void* k_pages, const void* v_pages,
+                            const float* k_scale, const float* v_scale, const int32_t* table,
+                            const int32_t* lengths, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, hs2_stream_t stream);
+
+/*
+ * Causal attention of a chunk of queries to a window of recent tokens and the
+ * first tokens (sinks): query i of sequence b sits at position t = Lk - Lq + i
+ * and sees the keys s <= t with s > t - window or s < n_sink.  Lq = Lk is a
+ * whole prompt, Lq = 1 a decode step over a bf16 cache, window >= Lk plain
+ * causal attention.
+ *   q [B, Lq, Hq, d] bf16, k, v [B, Lk, Hkv, d] bf16; Hq a multiple of Hkv, at
+ *   most 16 query heads per KV head (query head h reads KV head h / (Hq / Hkv))
+ *   o [B, Lq, Hq, d] bf16 out; lse [B, Lq, Hq] fp32 out (natural log), may be NULL
+ * A row that a query does not see never reaches its output, whatever it holds
+ * (the padding of a right-padded batch may be anything).
+ */
+typedef struct {
+    int B, Lq, Lk, Hq, Hkv, d, window, n_sink;
+    float scale;
+} hs2_window_shape;
+hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const void* k,
+                           const void* v, void* o, float* lse, hs2_stream_t stream);
+
 /* Size of the fixed device scratch used by hs2_decode_select_noalloc. */
 #define HS2_NOALLOC_SCRATCH_BYTES (96u << 20)
 

@@ -10,6 +10,13 @@ Entry points (same names as the C ABI):
   hs2_sparse_attn       sparse layer over the inherited selection (prefill)
   hs2_decode_select     decode full layer + selection, split over the cache
   hs2_decode_sparse     decode sparse layer over the inherited selection
+  hs2_kv_write, hs2_kv_read
+                        quantise K/V rows into the e4m3 cache that the decode
+                        layers read, and read them back
+  hs2_paged_kv_write, hs2_paged_kv_read, hs2_paged_decode
+                        the same for a paged cache with a scale per page and KV
+                        head, and the decode attention over it
+  hs2_window_attn       attention to a window of recent tokens and the first ones
 """
 from __future__ import annotations
 
@@ -41,7 +48,8 @@ EXPORTED = [
     "hs2_full_attn_select_blocks_workspace", "hs2_full_attn_select_blocks",
     "hs2_decode_stage_workspace", "hs2_decode_stage", "hs2_decode_sparse_staged",
     "hs2_full_attn", "hs2_select", "hs2_check_bounded_wait", "hs2_full_attn_rows",
-    "hs2_select_rows",
+    "hs2_select_rows", "hs2_kv_write", "hs2_kv_read", "hs2_paged_kv_write",
+    "hs2_paged_kv_read", "hs2_paged_decode_workspace", "hs2_paged_decode", "hs2_window_attn",
 ]
 
 
@@ -61,6 +69,21 @@ class DecodeShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Tmax", ctypes.c_int), ("Hq", ctypes.c_int),
                 ("d", ctypes.c_int), ("W", ctypes.c_int), ("k", ctypes.c_int),
                 ("scale", ctypes.c_float), ("kv", ctypes.c_int)]
+
+
+class CacheShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Tmax", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class WindowShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Lq", ctypes.c_int), ("Lk", ctypes.c_int),
+                ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("window", ctypes.c_int), ("n_sink", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -115,6 +138,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.hs2_decode_sparse_staged.restype = i32
     L.hs2_selection_overlap.argtypes = [P, vp, vp, vp, vp, vp]
     L.hs2_selection_overlap.restype = i32
+    C, G, W = (ctypes.POINTER(x) for x in (CacheShape, PagedShape, WindowShape))
+    f32 = ctypes.c_float
+    L.hs2_kv_write.argtypes = [C, i32] + [vp] * 9
+    L.hs2_kv_write.restype = i32
+    L.hs2_kv_read.argtypes = [C, i32] + [vp] * 9
+    L.hs2_kv_read.restype = i32
+    L.hs2_paged_kv_write.argtypes = [G, i32] + [vp] * 10
+    L.hs2_paged_kv_write.restype = i32
+    L.hs2_paged_kv_read.argtypes = [G, i32] + [vp] * 10
+    L.hs2_paged_kv_read.restype = i32
+    L.hs2_paged_decode_workspace.argtypes = [G, i32]
+    L.hs2_paged_decode_workspace.restype = sz
+    L.hs2_paged_decode.argtypes = [G, i32, i32, i32, f32] + [vp] * 10 + [sz, vp]
+    L.hs2_paged_decode.restype = i32
+    L.hs2_window_attn.argtypes = [W, vp, vp, vp, vp, vp, vp]
+    L.hs2_window_attn.restype = i32
     L.hs2_check_bounded_wait.argtypes = [ctypes.c_uint, vp]
     L.hs2_check_bounded_wait.restype = i32
     L.hs2_get_last_device_error.argtypes = [vp]
@@ -463,6 +502,184 @@ def hs2_decode_sparse_staged(q, staged, Tmax: int, W: int, k_top: int, *, kv="e4
                                          _ptr(o, "o", _BF16, q.numel()), _stream(stream))
     _check(st, "hs2_decode_sparse_staged")
     return o
+
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_INT_MAX = 2**31 - 1
+
+
+def _dense(t, name: str, dtypes, shape, dev: int, optional: bool = False):
+    """Device pointer of a dense tensor of exactly this shape on device `dev`
+    (the checks of _ptr, with the shape instead of the element count)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous (dense, row-major)")
+    if t.get_device() != dev:
+        _check_device(name, t.device)
+    return t.data_ptr()
+
+
+def _rank(t, name: str, rank: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dim() != rank:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {rank}")
+    if not t.is_cuda:
+        _check_device(name, t.device)
+    return t.shape
+
+
+def _alloc(stream, shape, dtype, dev: int):
+    """Memory for a call on `stream` (None: the current one), from that
+    stream's pool, so that it is not reused before the call's kernels are done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def paged_shape(B, Hkv, d, page, n_pages, max_pages) -> PagedShape:
+    return PagedShape(B, Hkv, d, page, n_pages, max_pages)
+
+
+def hs2_kv_write(k_new, v_new, start, k_cache, v_cache, k_scale, v_scale, *, count=None,
+                 stream=None) -> None:
+    """Quantise K/V rows into the e4m3 token cache.  k_new, v_new [B,N,d] bf16;
+    start, count [B] int32; caches [B,Tmax,d] codes; scales [B,Tmax] fp32."""
+    B, N, d = _rank(k_new, "k_new", 3)
+    Tmax = _rank(k_cache, "k_cache", 3)[1]
+    dev = _current_device()
+    rows, cache, scales = (B, N, d), (B, Tmax, d), (B, Tmax)
+    st = load().hs2_kv_write(
+        CacheShape(B, Tmax, d), N, _dense(k_new, "k_new", _BF16, rows, dev),
+        _dense(v_new, "v_new", _BF16, rows, dev), _dense(start, "start", _I32, (B,), dev),
+        _dense(count, "count", _I32, (B,), dev, True),
+        _dense(k_cache, "k_cache", _E4M3, cache, dev), _dense(v_cache, "v_cache", _E4M3, cache, dev),
+        _dense(k_scale, "k_scale", _F32, scales, dev), _dense(v_scale, "v_scale", _F32, scales, dev),
+        _stream(stream))
+    _check(st, "hs2_kv_write")
+
+
+def hs2_kv_read(k_cache, v_cache, k_scale, v_scale, start, N: int, *, count=None, k=None, v=None,
+                stream=None):
+    """Read N rows per sequence of the e4m3 token cache back.  Returns (k, v) [B,N,d] bf16."""
+    B, Tmax, d = _rank(k_cache, "k_cache", 3)
+    dev = _current_device()
+    rows, cache, scales = (B, N, d), (B, Tmax, d), (B, Tmax)
+    k = _alloc(stream, rows, torch.bfloat16, dev) if k is None else k
+    v = _alloc(stream, rows, torch.bfloat16, dev) if v is None else v
+    st = load().hs2_kv_read(
+        CacheShape(B, Tmax, d), N, _dense(k_cache, "k_cache", _E4M3, cache, dev),
+        _dense(v_cache, "v_cache", _E4M3, cache, dev), _dense(k_scale, "k_scale", _F32, scales, dev),
+        _dense(v_scale, "v_scale", _F32, scales, dev), _dense(start, "start", _I32, (B,), dev),
+        _dense(count, "count", _I32, (B,), dev, True), _dense(k, "k", _BF16, rows, dev),
+        _dense(v, "v", _BF16, rows, dev), _stream(stream))
+    _check(st, "hs2_kv_read")
+    return k, v
+
+
+def _paged(k_pages, v_pages, k_scale, v_scale, table, dev):
+    """The shape of a paged cache and the pointers of its five tensors."""
+    P, Hkv, page, d = pages = _rank(k_pages, "k_pages", 4)
+    B, mp = _rank(table, "table", 2)
+    return PagedShape(B, Hkv, d, page, P, mp), (
+        _dense(k_pages, "k_pages", _E4M3, pages, dev), _dense(v_pages, "v_pages", _E4M3, pages, dev),
+        _dense(k_scale, "k_scale", _F32, (P, Hkv), dev),
+        _dense(v_scale, "v_scale", _F32, (P, Hkv), dev), _dense(table, "table", _I32, (B, mp), dev))
+
+
+def hs2_paged_kv_write(k_new, v_new, table, start, k_pages, v_pages, k_scale, v_scale, *,
+                       count=None, stream=None) -> None:
+    """Quantise K/V rows into the paged e4m3 cache.  k_new, v_new [B,N,Hkv,d]
+    bf16; table [B,max_pages], start, count [B] int32; pages [P,Hkv,page,d]
+    codes; scales [P,Hkv] fp32."""
+    dev = _current_device()
+    shape, (kp, vp, ks, vs, tb) = _paged(k_pages, v_pages, k_scale, v_scale, table, dev)
+    B = shape.B
+    N = _rank(k_new, "k_new", 4)[1]
+    rows = (B, N, shape.Hkv, shape.d)
+    st = load().hs2_paged_kv_write(
+        shape, N, _dense(k_new, "k_new", _BF16, rows, dev), _dense(v_new, "v_new", _BF16, rows, dev),
+        tb, _dense(start, "start", _I32, (B,), dev), _dense(count, "count", _I32, (B,), dev, True),
+        kp, vp, ks, vs, _stream(stream))
+    _check(st, "hs2_paged_kv_write")
+
+
+def hs2_paged_kv_read(k_pages, v_pages, k_scale, v_scale, table, start, N: int, *, count=None,
+                      k=None, v=None, stream=None):
+    """Read N rows per sequence of the paged e4m3 cache back.  Returns (k, v) [B,N,Hkv,d] bf16."""
+    dev = _current_device()
+    shape, ptrs = _paged(k_pages, v_pages, k_scale, v_scale, table, dev)
+    B = shape.B
+    rows = (B, N, shape.Hkv, shape.d)
+    k = _alloc(stream, rows, torch.bfloat16, dev) if k is None else k
+    v = _alloc(stream, rows, torch.bfloat16, dev) if v is None else v
+    st = load().hs2_paged_kv_read(
+        shape, N, *ptrs, _dense(start, "start", _I32, (B,), dev),
+        _dense(count, "count", _I32, (B,), dev, True), _dense(k, "k", _BF16, rows, dev),
+        _dense(v, "v", _BF16, rows, dev), _stream(stream))
+    _check(st, "hs2_paged_kv_read")
+    return k, v
+
+
+def hs2_paged_decode_workspace(shape: PagedShape, Hq: int) -> int:
+    return load().hs2_paged_decode_workspace(ctypes.byref(shape), Hq)
+
+
+def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, window=None,
+                     n_sink: int = 0, scale=None, o=None, lse=None, workspace=None,
+                     want_lse: bool = True, stream=None):
+    """Decode attention over the paged e4m3 cache.  q [B,Hq,d] bf16; lengths [B]
+    int32; window None: all positions.  Returns (o, lse or None)."""
+    dev = _current_device()
+    shape, ptrs = _paged(k_pages, v_pages, k_scale, v_scale, table, dev)
+    B, Hq, d = _rank(q, "q", 3)
+    out = (shape.B, Hq, shape.d)
+    o = _alloc(stream, out, torch.bfloat16, dev) if o is None else o
+    if lse is None and want_lse:
+        lse = _alloc(stream, out[:2], torch.float32, dev)
+    lib = load()
+    if workspace is None:
+        workspace = _alloc(stream, max(16, lib.hs2_paged_decode_workspace(shape, Hq)),
+                           torch.uint8, dev)
+    st = lib.hs2_paged_decode(
+        shape, Hq, _INT_MAX if window is None else min(window, _INT_MAX), min(n_sink, _INT_MAX),
+        1.0 / math.sqrt(d) if scale is None else scale, _dense(q, "q", _BF16, out, dev), *ptrs,
+        _dense(lengths, "lengths", _I32, (shape.B,), dev), _dense(o, "o", _BF16, out, dev),
+        _dense(lse, "lse", _F32, out[:2], dev, True),
+        _dense(workspace, "workspace", (workspace.dtype,), workspace.shape, dev),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "hs2_paged_decode")
+    return o, lse
+
+
+def hs2_window_attn(q, k, v, window: int, n_sink: int = 0, *, scale=None, o=None, lse=None,
+                    want_lse: bool = True, stream=None):
+    """Causal attention to the last `window` tokens and the first n_sink.
+    q [B,Lq,Hq,d], k/v [B,Lk,Hkv,d] bf16, query i at position Lk - Lq + i.
+    Returns (o, lse or None)."""
+    dev = _current_device()
+    B, Lq, Hq, d = rows = _rank(q, "q", 4)
+    _, Lk, Hkv, _ = _rank(k, "k", 4)
+    keys = (B, Lk, Hkv, d)
+    o = _alloc(stream, rows, torch.bfloat16, dev) if o is None else o
+    if lse is None and want_lse:
+        lse = _alloc(stream, rows[:3], torch.float32, dev)
+    shape = WindowShape(B, Lq, Lk, Hq, Hkv, d, min(window, _INT_MAX), min(n_sink, _INT_MAX),
+                        1.0 / math.sqrt(d) if scale is None else scale)
+    st = load().hs2_window_attn(
+        shape, _dense(q, "q", _BF16, rows, dev), _dense(k, "k", _BF16, keys, dev),
+        _dense(v, "v", _BF16, keys, dev), _dense(o, "o", _BF16, rows, dev),
+        _dense(lse, "lse", _F32, rows[:3], dev, True), _stream(stream))
+    _check(st, "hs2_window_attn")
+    return o, lse
 
 
 def hs2_check_bounded_wait(limit_us: int = 1000, stream=None) -> None:

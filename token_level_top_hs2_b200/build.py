@@ -1,6 +1,6 @@
 """Build the hs2 CUDA library (sm_100a) in-tree: token_level_top_hs2_b200/libhs2.so.
 
-One nvcc invocation over the single translation unit csrc/hs2_api.cu; the
+One nvcc invocation over the translation units csrc/*_api.cu; the
 CUDA runtime is linked statically so the library carries no runtime-version
 dependency of its own.
 """
@@ -19,7 +19,9 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-warn-spills",
+    "--threads", "2",
 ]
+UNITS = ["hs2_api.cu", "cache_api.cu"]
 
 
 def sources():
@@ -34,7 +36,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             return OUT
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "hs2_api.cu"), "-o", OUT + ".tmp"]
+           *[os.path.join(CSRC, u) for u in UNITS], "-o", OUT + ".tmp"]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd))

@@ -1,0 +1,230 @@
+// C ABI of the cache and window operators (declared in include/hs2.h): the
+// e4m3 caches' writers and readers, the paged decode attention and the window
+// attention.  Argument validation and launches; the kernels live in the headers.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "host.cuh"
+#include "kv_cache.cuh"
+#include "paged_decode.cuh"
+#include "window_attn.cuh"
+
+using namespace hs2;
+
+namespace {
+
+constexpr int kMaxGroup = 16;  // query heads per KV head
+constexpr int kMaxHeads = 4096;
+
+bool scale_ok(float s) { return s > 0.f && isfinite(s); }
+
+template <class... P>
+bool pointers_ok(const P*... p) {
+    return ((p != nullptr && aligned16(p)) && ...);
+}
+
+hs2_status check_cache(const hs2_cache_shape* s) {
+    if (!s) return HS2_ERR_INVALID_ARG;
+    if (s->B < 1 || s->B > 65535 || s->Tmax < 1) return HS2_ERR_INVALID_ARG;
+    if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
+    return HS2_OK;
+}
+
+hs2_status check_paged(const hs2_paged_shape* s) {
+    if (!s) return HS2_ERR_INVALID_ARG;
+    if (s->B < 1 || s->B > 65535 || s->Hkv < 1 || s->page < 1 || s->n_pages < 1 || s->max_pages < 1)
+        return HS2_ERR_INVALID_ARG;
+    if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
+    if (s->page != 16 && s->page != 32 && s->page != 64 && s->page != 128)
+        return HS2_ERR_UNSUPPORTED;
+    if (s->Hkv > kMaxHeads) return HS2_ERR_UNSUPPORTED;
+    // positions, and (page, head) numbers, are 32-bit
+    if ((int64_t)s->max_pages * s->page > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    if ((int64_t)s->n_pages * s->Hkv > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    return HS2_OK;
+}
+
+hs2_status check_groups(int Hq, int Hkv) {
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv) return HS2_ERR_INVALID_ARG;
+    if (Hq / Hkv > kMaxGroup || Hkv > kMaxHeads) return HS2_ERR_UNSUPPORTED;
+    return HS2_OK;
+}
+
+template <int D>
+hs2_status launch_page_write(const hs2_paged_shape* s, int N, const void* k_new, const void* v_new,
+                             const int32_t* table, const int32_t* start, const int32_t* count,
+                             void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                             cudaStream_t st, unsigned* flags) {
+    // pages that N rows can touch, wherever they start
+    const int64_t slots = ((int64_t)N + s->page - 2) / s->page + 1;
+    const int64_t blocks = slots * s->Hkv * 2;
+    if (blocks > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    auto run = [&](auto kern) {
+        kern<<<dim3((unsigned)blocks, s->B), kvc::kPageThreads, 0, st>>>(
+            static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
+            table, start, count, static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
+            k_scale, v_scale, N, s->Hkv, s->n_pages, s->max_pages, flags);
+        return launch_status();
+    };
+    switch (s->page) {
+        case 16: return run(kvc::paged_write_kernel<D, 16>);
+        case 32: return run(kvc::paged_write_kernel<D, 32>);
+        case 64: return run(kvc::paged_write_kernel<D, 64>);
+        default: return run(kvc::paged_write_kernel<D, 128>);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+hs2_status hs2_kv_write(const hs2_cache_shape* shape, int N, const void* k_new, const void* v_new,
+                        const int32_t* start, const int32_t* count, void* k_cache, void* v_cache,
+                        float* k_scale, float* v_scale, hs2_stream_t stream) {
+    hs2_status e = check_cache(shape);
+    if (e != HS2_OK) return e;
+    if (N < 1 || N > shape->Tmax) return HS2_ERR_INVALID_ARG;
+    if (!pointers_ok(k_new, v_new, start, k_cache, v_cache, k_scale, v_scale) || !aligned16(count))
+        return HS2_ERR_INVALID_ARG;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int rows = 256 / (shape->d / 8) * kvc::kTokRows;
+    const dim3 grid((N + rows - 1) / rows, shape->B);
+    auto run = [&](auto kern) {
+        kern<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(k_new),
+                                   static_cast<const __nv_bfloat16*>(v_new), start, count,
+                                   static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
+                                   k_scale, v_scale, N, shape->Tmax, flags);
+        return launch_status();
+    };
+    return shape->d == 128 ? run(kvc::token_write_kernel<128>) : run(kvc::token_write_kernel<64>);
+}
+
+hs2_status hs2_kv_read(const hs2_cache_shape* shape, int N, const void* k_cache, const void* v_cache,
+                       const float* k_scale, const float* v_scale, const int32_t* start,
+                       const int32_t* count, void* k, void* v, hs2_stream_t stream) {
+    hs2_status e = check_cache(shape);
+    if (e != HS2_OK) return e;
+    if (N < 1 || N > shape->Tmax) return HS2_ERR_INVALID_ARG;
+    if (!pointers_ok(k_cache, v_cache, k_scale, v_scale, start, k, v) || !aligned16(count))
+        return HS2_ERR_INVALID_ARG;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int rows = 256 / (shape->d / 16);
+    const dim3 grid((N + rows - 1) / rows, shape->B);
+    auto run = [&](auto kern) {
+        kern<<<grid, 256, 0, st>>>(static_cast<const uint8_t*>(k_cache),
+                                   static_cast<const uint8_t*>(v_cache), k_scale, v_scale, start,
+                                   count, static_cast<__nv_bfloat16*>(k),
+                                   static_cast<__nv_bfloat16*>(v), N, shape->Tmax, flags);
+        return launch_status();
+    };
+    return shape->d == 128 ? run(kvc::token_read_kernel<128>) : run(kvc::token_read_kernel<64>);
+}
+
+hs2_status hs2_paged_kv_write(const hs2_paged_shape* shape, int N, const void* k_new,
+                              const void* v_new, const int32_t* table, const int32_t* start,
+                              const int32_t* count, void* k_pages, void* v_pages, float* k_scale,
+                              float* v_scale, hs2_stream_t stream) {
+    hs2_status e = check_paged(shape);
+    if (e != HS2_OK) return e;
+    if (N < 1 || N > shape->max_pages * shape->page) return HS2_ERR_INVALID_ARG;
+    if (!pointers_ok(k_new, v_new, table, start, k_pages, v_pages, k_scale, v_scale) ||
+        !aligned16(count))
+        return HS2_ERR_INVALID_ARG;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (shape->d == 128)
+        return launch_page_write<128>(shape, N, k_new, v_new, table, start, count, k_pages, v_pages,
+                                      k_scale, v_scale, st, flags);
+    return launch_page_write<64>(shape, N, k_new, v_new, table, start, count, k_pages, v_pages,
+                                 k_scale, v_scale, st, flags);
+}
+
+hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_pages,
+                             const void* v_pages, const float* k_scale, const float* v_scale,
+                             const int32_t* table, const int32_t* start, const int32_t* count,
+                             void* k, void* v, hs2_stream_t stream) {
+    hs2_status e = check_paged(shape);
+    if (e != HS2_OK) return e;
+    if (N < 1 || N > shape->max_pages * shape->page) return HS2_ERR_INVALID_ARG;
+    if (!pointers_ok(k_pages, v_pages, k_scale, v_scale, table, start, k, v) || !aligned16(count))
+        return HS2_ERR_INVALID_ARG;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t blocks = ((int64_t)N * shape->Hkv * (shape->d / 16) + 255) / 256;
+    if (blocks > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    auto run = [&](auto kern) {
+        kern<<<dim3((unsigned)blocks, shape->B), 256, 0, st>>>(
+            static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(v_pages), k_scale,
+            v_scale, table, start, count, static_cast<__nv_bfloat16*>(k),
+            static_cast<__nv_bfloat16*>(v), N, shape->Hkv, shape->page, shape->n_pages,
+            shape->max_pages, flags);
+        return launch_status();
+    };
+    return shape->d == 128 ? run(kvc::paged_read_kernel<128>) : run(kvc::paged_read_kernel<64>);
+}
+
+size_t hs2_paged_decode_workspace(const hs2_paged_shape* shape, int Hq) {
+    if (check_paged(shape) != HS2_OK || check_groups(Hq, shape->Hkv) != HS2_OK) return 0;
+    return 16;
+}
+
+hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, int n_sink,
+                            float scale, const void* q, const void* k_pages, const void* v_pages,
+                            const float* k_scale, const float* v_scale, const int32_t* table,
+                            const int32_t* lengths, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, hs2_stream_t stream) {
+    hs2_status e = check_paged(shape);
+    if (e != HS2_OK) return e;
+    e = check_groups(Hq, shape->Hkv);
+    if (e != HS2_OK) return e;
+    if (window < 1 || n_sink < 0 || !scale_ok(scale)) return HS2_ERR_INVALID_ARG;
+    if (!pointers_ok(q, k_pages, v_pages, k_scale, v_scale, table, lengths, o) || !aligned16(lse) ||
+        !pointers_ok(workspace))
+        return HS2_ERR_INVALID_ARG;
+    if (workspace_bytes < hs2_paged_decode_workspace(shape, Hq)) return HS2_ERR_WORKSPACE;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    auto run = [&](auto kern) {
+        kern<<<dim3(Hq, shape->B), 32, 0, st>>>(
+            static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_pages),
+            static_cast<const uint8_t*>(v_pages), k_scale, v_scale, table, lengths,
+            static_cast<__nv_bfloat16*>(o), lse, Hq, shape->Hkv, shape->page, shape->n_pages,
+            shape->max_pages, window, n_sink, scale * kLog2e, flags);
+        return launch_status();
+    };
+    return shape->d == 128 ? run(pgd::paged_rows_kernel<128>) : run(pgd::paged_rows_kernel<64>);
+}
+
+hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const void* k,
+                           const void* v, void* o, float* lse, hs2_stream_t stream) {
+    const hs2_window_shape* s = shape;
+    if (!s) return HS2_ERR_INVALID_ARG;
+    if (s->B < 1 || s->B > 65535 || s->Lq < 1 || s->Lk < s->Lq || s->window < 1 || s->n_sink < 0 ||
+        !scale_ok(s->scale))
+        return HS2_ERR_INVALID_ARG;
+    hs2_status e = check_groups(s->Hq, s->Hkv);
+    if (e != HS2_OK) return e;
+    if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
+    if (!pointers_ok(q, k, v, o) || !aligned16(lse)) return HS2_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t blocks = ((int64_t)s->B * s->Lq * s->Hq + 3) / 4;
+    if (blocks > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    auto run = [&](auto kern) {
+        kern<<<(unsigned)blocks, 128, 0, st>>>(
+            static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse, s->B, s->Lq,
+            s->Lk, s->Hq, s->Hkv, s->window, s->n_sink, s->scale * kLog2e);
+        return launch_status();
+    };
+    return s->d == 128 ? run(win::window_rows_kernel<128>) : run(win::window_rows_kernel<64>);
+}
+
+}  // extern "C"

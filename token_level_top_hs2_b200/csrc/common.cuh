@@ -30,6 +30,7 @@ enum : unsigned {
     FLAG_BAD_INDEX = 4u,    // a selection index outside [0, t]
     FLAG_SCALE_RANGE = 8u,  // a V scale beyond 255 on an e4m3 path
     FLAG_TIMEOUT = 16u,     // a bounded wait inside a kernel gave up
+    FLAG_NONFINITE = 32u,   // an infinity or NaN among the rows to quantise
 };
 
 HS2_DEV uint32_t lane_id() { return threadIdx.x & 31; }

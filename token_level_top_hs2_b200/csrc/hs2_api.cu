@@ -1,6 +1,7 @@
 // C ABI of the hs2 library (declared in include/hs2.h): argument validation,
-// workspace layout and kernel launches.  All kernels live in the headers
-// included below; this file is the library's single translation unit.
+// workspace layout and kernel launches of the selection layers and what goes
+// with them.  The kernels live in the headers included below; the cache and
+// window operators are the library's other translation unit, cache_api.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -20,6 +21,7 @@
 #include "stage.cuh"
 #include "prefill_tc.cuh"
 #include "sparse_kernels.cuh"
+#include "host.cuh"
 
 using namespace hs2;
 
@@ -34,7 +36,9 @@ unsigned* g_flag_ptr[kMaxDevices];
 // threads may make their first calls on a device at the same time
 std::mutex g_addr_mutex;
 
-unsigned* device_flags() {
+}  // namespace
+
+unsigned* hs2::device_flags() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
     std::lock_guard<std::mutex> lock(g_addr_mutex);
@@ -46,8 +50,7 @@ unsigned* device_flags() {
     return g_flag_ptr[dev];
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
 
 hs2_status check_common(int Hq, int d, int W, int k, float scale) {
     if (!(scale > 0.f) || !isfinite(scale) || W < 1 || k < 0) return HS2_ERR_INVALID_ARG;
@@ -68,68 +71,6 @@ hs2_status check_decode(const hs2_decode_shape* s) {
     if (s->B < 1 || s->Tmax < 1 || s->B > 65535) return HS2_ERR_INVALID_ARG;
     if (s->kv != HS2_KV_BF16 && s->kv != HS2_KV_E4M3) return HS2_ERR_INVALID_ARG;
     return check_common(s->Hq, s->d, s->W, s->k, s->scale);
-}
-
-hs2_status launch_status() {
-    return cudaGetLastError() == cudaSuccess ? HS2_OK : HS2_ERR_CUDA;
-}
-
-// Raise a kernel's dynamic shared-memory limit once per (kernel, device) and
-// size increase, so repeated calls -- including calls under stream capture --
-// make no further attribute calls.
-struct SmemLimit {
-    const void* fn;
-    int dev;
-    size_t bytes;
-};
-SmemLimit g_smem_limits[512];
-int g_n_smem_limits = 0;
-std::mutex g_smem_mutex;
-
-template <class K>
-bool set_smem(K kernel, size_t bytes) {
-    // (static + dynamic shared memory above 48 KiB needs the opt-in, so any
-    // nonzero request is registered; the table makes it once per kernel/device)
-    if (bytes == 0) return true;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const void* fn = reinterpret_cast<const void*>(kernel);
-    std::lock_guard<std::mutex> lock(g_smem_mutex);
-    SmemLimit* e = nullptr;
-    for (int i = 0; i < g_n_smem_limits; i++)
-        if (g_smem_limits[i].fn == fn && g_smem_limits[i].dev == dev) e = &g_smem_limits[i];
-    if (e && e->bytes >= bytes) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-        return false;
-    if (!e) {
-        if (g_n_smem_limits == 512) return true;  // table full: set again next time
-        e = &g_smem_limits[g_n_smem_limits++];
-        e->fn = fn;
-        e->dev = dev;
-    }
-    e->bytes = bytes;
-    return true;
-}
-
-// Launch with programmatic stream serialisation: the kernel may start while
-// the previous kernel of the stream drains (its prologue overlaps that
-// kernel's tail); it calls griddep_wait() before reading that kernel's
-// results.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 // Check of the error path every pipelined kernel shares: one thread waits on
@@ -153,34 +94,6 @@ __global__ void zero16_kernel(uint4* __restrict__ p, int n16) {
     griddep_launch();
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += gridDim.x * blockDim.x)
         p[i] = make_uint4(0u, 0u, 0u, 0u);
-}
-
-// ------------------------------------------------------------ tensor maps
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no direct
-// libcuda link).  bf16 tensors, 128-byte swizzle, 64-element inner box.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-bool map_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides, const cuuint32_t* box) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides,
-               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Q [B, L, Hq, D]: box of `rows` positions x 64 columns of one head.

@@ -1,0 +1,298 @@
+// Writers and readers of the 8-bit K/V caches.
+//
+//   token cache   codes [B, Tmax, d], one fp32 scale per token:
+//                 s = max|x| / 448 (1 for a row of zeros), code = e4m3(x / s)
+//   paged cache   pages [P, Hkv, page, d], one scale per page and KV head, a
+//                 power of two: the least s >= 2^-126 with max|x| <= 448 s
+//
+// e4m3 rounding is to nearest even, saturated to +-448.  A page's scale is a
+// power of two so that a page that is appended to can raise it and re-round
+// its older codes without a second rounding: code * 2^-n is exact unless it
+// falls below 2^-6, where e4m3 has a fixed step.  It costs less than one of
+// e4m3's 17 octaves of range and no precision inside it.
+//
+// All of these move bytes once: a write reads 2 bytes and stores 1 per
+// element, a read the reverse.
+#pragma once
+
+#include "common.cuh"
+
+namespace hs2 {
+namespace kvc {
+
+constexpr float kE4m3Max = 448.f;
+
+// Two floats -> two e4m3 codes (lo in bits 0..7), nearest even, saturated.
+HS2_DEV uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Largest |x| of the eight bf16 values of w, as bf16 bits (they order like the
+// magnitudes), non-finite values left out; *bad is set if there are any.
+HS2_DEV uint32_t amax_bits(uint4 w, bool* bad) {
+    const uint32_t a0 = w.x & 0x7FFF7FFFu, a1 = w.y & 0x7FFF7FFFu;
+    const uint32_t a2 = w.z & 0x7FFF7FFFu, a3 = w.w & 0x7FFF7FFFu;
+    const uint32_t m = __vmaxu2(__vmaxu2(a0, a1), __vmaxu2(a2, a3));
+    uint32_t r = max(m & 0xFFFFu, m >> 16);
+    if (r >= 0x7F80u) {
+        *bad = true;
+        r = 0;
+        const uint32_t a[4] = {a0, a1, a2, a3};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t lo = a[i] & 0xFFFFu, hi = a[i] >> 16;
+            if (lo < 0x7F80u) r = max(r, lo);
+            if (hi < 0x7F80u) r = max(r, hi);
+        }
+    }
+    return r;
+}
+
+// The least power of two s >= 2^-126 with top <= 448 s (top >= 0, finite; 448
+// is 1.75 * 2^8, so the answer is read off top's exponent and whether its
+// significand exceeds 1.75).
+HS2_DEV float page_scale(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)max(e, 1) << 23);  // a subnormal or zero top gives 2^-126
+}
+
+// ------------------------------------------------------------- token cache
+// One group of D/8 lanes per row, eight elements a lane; each group takes the
+// K and the V row of kRows tokens, all loads in flight together.
+constexpr int kTokRows = 2;
+
+template <int D>
+__global__ void __launch_bounds__(256)
+token_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
+                   const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+                   uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
+                   float* __restrict__ k_scale, float* __restrict__ v_scale, int N, int Tmax,
+                   unsigned* __restrict__ flags) {
+    constexpr int LPR = D / 8;         // lanes per row
+    constexpr int RPB = 256 / LPR;     // rows per block and step
+    const int b = blockIdx.y;
+    const int lane = threadIdx.x % LPR;
+    const int s0 = start[b], n = count ? count[b] : N;
+    if (n < 0 || n > N || s0 < 0 || s0 > Tmax - n) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+        return;
+    }
+    const int i0 = blockIdx.x * (RPB * kTokRows) + threadIdx.x / LPR;
+    uint4 w[2 * kTokRows];
+#pragma unroll
+    for (int r = 0; r < kTokRows; r++) {
+        const int i = i0 + r * RPB;
+        const size_t src = ((size_t)b * N + i) * D + lane * 8;
+        w[2 * r] = i < n ? ldg_stream(k_new + src) : make_uint4(0, 0, 0, 0);
+        w[2 * r + 1] = i < n ? ldg_stream(v_new + src) : make_uint4(0, 0, 0, 0);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 2 * kTokRows; j++) {
+        const int i = i0 + (j >> 1) * RPB;
+        uint32_t top = amax_bits(w[j], &bad);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        const float s = top ? __uint_as_float(top << 16) / kE4m3Max : 1.f;
+        const uint32_t c0 = e4m3x2(bf16_lo(w[j].x) / s, bf16_hi(w[j].x) / s);
+        const uint32_t c1 = e4m3x2(bf16_lo(w[j].y) / s, bf16_hi(w[j].y) / s);
+        const uint32_t c2 = e4m3x2(bf16_lo(w[j].z) / s, bf16_hi(w[j].z) / s);
+        const uint32_t c3 = e4m3x2(bf16_lo(w[j].w) / s, bf16_hi(w[j].w) / s);
+        if (i < n) {
+            const size_t row = (size_t)b * Tmax + s0 + i;
+            *reinterpret_cast<uint2*>((j & 1 ? v_cache : k_cache) + row * D + lane * 8) =
+                make_uint2(c0 | c1 << 16, c2 | c3 << 16);
+            if (lane == 0) (j & 1 ? v_scale : k_scale)[row] = s;
+        }
+    }
+    if (bad) atomicOr(flags, FLAG_NONFINITE);
+}
+
+// Sixteen codes and their scale -> sixteen bf16 (rounded to nearest even once:
+// code and scale multiply exactly enough in fp32, whose rounding of the
+// product is 2^-24 relative, far below bf16's).
+HS2_DEV void dequant16(uint4 c, float s, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 a = f16x2_to_float2(e4m3x2_lo_to_f16x2(w[i]));
+        const float2 b = f16x2_to_float2(e4m3x2_lo_to_f16x2(w[i] >> 16));
+        r[2 * i] = pack_bf16(a.x * s, a.y * s);
+        r[2 * i + 1] = pack_bf16(b.x * s, b.y * s);
+    }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+token_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
+                  const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+                  const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+                  __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v, int N, int Tmax,
+                  unsigned* __restrict__ flags) {
+    constexpr int LPR = D / 16;
+    constexpr int RPB = 256 / LPR;
+    const int b = blockIdx.y;
+    const int lane = threadIdx.x % LPR;
+    const int s0 = start[b], n = count ? count[b] : N;
+    if (n < 0 || n > N || s0 < 0 || s0 > Tmax - n) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+        return;
+    }
+    const int i = blockIdx.x * RPB + threadIdx.x / LPR;
+    if (i >= n) return;
+    const size_t row = (size_t)b * Tmax + s0 + i;
+    const uint4 ck = ldg_stream(k_cache + row * D + lane * 16);
+    const uint4 cv = ldg_stream(v_cache + row * D + lane * 16);
+    const float sk = k_scale[row], sv = v_scale[row];
+    const size_t dst = ((size_t)b * N + i) * D + lane * 16;
+    uint4 lo, hi;
+    dequant16(ck, sk, lo, hi);
+    reinterpret_cast<uint4*>(k + dst)[0] = lo;
+    reinterpret_cast<uint4*>(k + dst)[1] = hi;
+    dequant16(cv, sv, lo, hi);
+    reinterpret_cast<uint4*>(v + dst)[0] = lo;
+    reinterpret_cast<uint4*>(v + dst)[1] = hi;
+}
+
+// ------------------------------------------------------------- paged cache
+// One block per (touched page, KV head, K or V) and sequence; the page's new
+// rows stay in registers between the search for their largest magnitude and
+// the rounding, so they are read once.  grid (pages * Hkv * 2, B).
+constexpr int kPageThreads = 128;
+
+template <int D, int PAGE>
+__global__ void __launch_bounds__(kPageThreads)
+paged_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
+                   const int32_t* __restrict__ table, const int32_t* __restrict__ start,
+                   const int32_t* __restrict__ count, uint8_t* __restrict__ k_pages,
+                   uint8_t* __restrict__ v_pages, float* __restrict__ k_scale,
+                   float* __restrict__ v_scale, int N, int Hkv, int n_pages, int max_pages,
+                   unsigned* __restrict__ flags) {
+    constexpr int LPR = D / 8;                                      // lanes per row
+    constexpr int UNITS = PAGE * LPR;                               // 16-byte pieces of new rows
+    constexpr int U = (UNITS + kPageThreads - 1) / kPageThreads;    // a thread's pieces
+    __shared__ uint32_t s_top[kPageThreads / 32];
+    const int b = blockIdx.y, tid = threadIdx.x;
+    const int which = blockIdx.x & 1;
+    const int h = (blockIdx.x >> 1) % Hkv;
+    const int s0 = start[b], n = count ? count[b] : N;
+    if (n < 0 || n > N || s0 < 0 || s0 > max_pages * PAGE - n) {
+        if (blockIdx.x == 0 && tid == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+        return;
+    }
+    const int slot = s0 / PAGE + (int)(blockIdx.x >> 1) / Hkv;
+    const int p0 = max(0, s0 - slot * PAGE), p1 = min(PAGE, s0 + n - slot * PAGE);
+    if (p0 >= p1) return;  // the rows do not reach this page
+    const int pid = table[(size_t)b * max_pages + slot];
+    if (pid < 0 || pid >= n_pages) {
+        if (tid == 0) atomicOr(flags, FLAG_BAD_INDEX);
+        return;
+    }
+    const __nv_bfloat16* src = which ? v_new : k_new;
+    const size_t ph = (size_t)pid * Hkv + h;
+    uint8_t* dst = (which ? v_pages : k_pages) + ph * (PAGE * D);
+    float* scale = (which ? v_scale : k_scale) + ph;
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int unit = u * kPageThreads + tid, r = unit / LPR;
+        const bool in = r >= p0 && r < p1;
+        const size_t i = (size_t)b * N + (slot * PAGE + r - s0);
+        w[u] = in ? ldg_stream(src + (i * Hkv + h) * D + (unit % LPR) * 8) : make_uint4(0, 0, 0, 0);
+    }
+    const float had = p0 > 0 ? *scale : 0.f;
+    bool bad = false;
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < U; u++) top = max(top, amax_bits(w[u], &bad));
+    top = __reduce_max_sync(~0u, top);
+    if ((tid & 31) == 0) s_top[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPageThreads / 32; i++) top = max(top, s_top[i]);
+    float s = page_scale(__uint_as_float(top << 16));
+    if (p0 > 0) {
+        if (had > 0.f && had < INFINITY) {
+            if (s > had) {
+                // the older rows' codes under the raised scale
+                const float f = had / s;
+                for (int unit = tid; unit < p0 * (D / 4); unit += kPageThreads) {
+                    uint32_t* c = reinterpret_cast<uint32_t*>(dst) + unit;
+                    const uint32_t old = *c;
+                    const float2 a = f16x2_to_float2(e4m3x2_lo_to_f16x2(old));
+                    const float2 e = f16x2_to_float2(e4m3x2_lo_to_f16x2(old >> 16));
+                    *c = e4m3x2(a.x * f, a.y * f) | e4m3x2(e.x * f, e.y * f) << 16;
+                }
+            } else {
+                s = had;
+            }
+        } else if (tid == 0) {
+            atomicOr(flags, FLAG_SCALE_RANGE);
+        }
+    }
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int unit = u * kPageThreads + tid, r = unit / LPR;
+        if (r >= p0 && r < p1) {
+            const uint32_t c0 = e4m3x2(bf16_lo(w[u].x) * inv, bf16_hi(w[u].x) * inv);
+            const uint32_t c1 = e4m3x2(bf16_lo(w[u].y) * inv, bf16_hi(w[u].y) * inv);
+            const uint32_t c2 = e4m3x2(bf16_lo(w[u].z) * inv, bf16_hi(w[u].z) * inv);
+            const uint32_t c3 = e4m3x2(bf16_lo(w[u].w) * inv, bf16_hi(w[u].w) * inv);
+            *reinterpret_cast<uint2*>(dst + (size_t)unit * 8) = make_uint2(c0 | c1 << 16, c2 | c3 << 16);
+        }
+    }
+    if (tid == 0) *scale = s;
+    if (bad) atomicOr(flags, FLAG_NONFINITE);
+}
+
+// Rows [start, start + count) of each sequence, every KV head: a thread takes
+// one 16-code piece of K and of V.  grid (pieces / 256, B).
+template <int D>
+__global__ void __launch_bounds__(256)
+paged_read_kernel(const uint8_t* __restrict__ k_pages, const uint8_t* __restrict__ v_pages,
+                  const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+                  const int32_t* __restrict__ table, const int32_t* __restrict__ start,
+                  const int32_t* __restrict__ count, __nv_bfloat16* __restrict__ k,
+                  __nv_bfloat16* __restrict__ v, int N, int Hkv, int page, int n_pages,
+                  int max_pages, unsigned* __restrict__ flags) {
+    constexpr int LPR = D / 16;
+    const int b = blockIdx.y;
+    const int s0 = start[b], n = count ? count[b] : N;
+    if (n < 0 || n > N || s0 < 0 || s0 > max_pages * page - n) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+        return;
+    }
+    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int lane = (int)(unit % LPR);
+    const int64_t row = unit / LPR;
+    const int i = (int)(row / Hkv), h = (int)(row % Hkv);
+    if (i >= n) return;
+    const int pos = s0 + i;
+    const int pid = table[(size_t)b * max_pages + pos / page];
+    if (pid < 0 || pid >= n_pages) {
+        atomicOr(flags, FLAG_BAD_INDEX);
+        return;
+    }
+    const size_t ph = (size_t)pid * Hkv + h;
+    const size_t at = (ph * page + pos % page) * D + lane * 16;
+    const uint4 ck = ldg_stream(k_pages + at), cv = ldg_stream(v_pages + at);
+    const float sk = k_scale[ph], sv = v_scale[ph];
+    const size_t dst = (((size_t)b * N + i) * Hkv + h) * D + lane * 16;
+    uint4 lo, hi;
+    dequant16(ck, sk, lo, hi);
+    reinterpret_cast<uint4*>(k + dst)[0] = lo;
+    reinterpret_cast<uint4*>(k + dst)[1] = hi;
+    dequant16(cv, sv, lo, hi);
+    reinterpret_cast<uint4*>(v + dst)[0] = lo;
+    reinterpret_cast<uint4*>(v + dst)[1] = hi;
+}
+
+}  // namespace kvc
+}  // namespace hs2
