@@ -127,8 +127,11 @@ def paged_decode(q, kvals, vvals, kscale, vscale, table, lengths, window, n_sink
         pos = np.arange(T)
         pos = pos[(pos >= T - window) | (pos < n_sink)]
         k, v = (paged_rows(z, s, table[b], page, pos) for z, s in ((kvals, kscale), (vvals, vscale)))
+        top = paged_rows(np.full_like(vvals, 448.0), vscale, table[b], page, pos)
         for h in range(Hkv):
-            out.append(attend(q[b, h * G:(h + 1) * G], k[:, h], v[:, h], sm_scale))
+            r = attend(q[b, h * G:(h + 1) * G], k[:, h], v[:, h], sm_scale)
+            r["vmax"] = np.full(d, top[:, h].max() if len(top) else 0.0)  # largest value a code can stand for
+            out.append(r)
     return _stack(out, G, d, (B, Hq))
 
 

@@ -19,6 +19,15 @@ constexpr int kMaxHeads = 4096;
 
 bool scale_ok(float s) { return s > 0.f && isfinite(s); }
 
+// SMs of the current device, at most one CTA of the persistent kernels each.
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return std::min(n, pgd::kMaxCtas);
+}
+
 template <class... P>
 bool pointers_ok(const P*... p) {
     return ((p != nullptr && aligned16(p)) && ...);
@@ -73,6 +82,71 @@ hs2_status launch_page_write(const hs2_paged_shape* s, int N, const void* k_new,
         case 64: return run(kvc::paged_write_kernel<D, 64>);
         default: return run(kvc::paged_write_kernel<D, 128>);
     }
+}
+
+// Pages [n_pages * Hkv, page, D] of e4m3 codes: a box is one page of one head.
+bool map_pages(CUtensorMap* m, const void* x, int64_t n, int page, int D) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page};
+    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)page, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(x), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct PagedCall {
+    const hs2_paged_shape* s;
+    const void *q, *k, *v;
+    const float *ks, *vs;
+    const int32_t *table, *lengths;
+    void* o;
+    float *lse, *part;
+    int G, window, n_sink;
+    float scale;
+    cudaStream_t st;
+    unsigned* flags;
+};
+
+template <int D, int NG>
+hs2_status run_paged(const PagedCall& c) {
+    const hs2_paged_shape* s = c.s;
+    CUtensorMap mk, mv;
+    const int64_t n = (int64_t)s->n_pages * s->Hkv;
+    if (!map_pages(&mk, c.k, n, s->page, D) || !map_pages(&mv, c.v, n, s->page, D))
+        return HS2_ERR_CUDA;
+    const int cap = s->max_pages * s->page;
+    const pgd::Work work = {c.lengths, s->B, cap, c.window, c.n_sink, s->Hkv};
+    // no more CTAs than tiles there can be
+    const int64_t seen = std::min<int64_t>(cap, (int64_t)c.window + c.n_sink);
+    const int64_t tiles = (seen / pgd::kTile + 3) * s->Hkv * s->B;
+    const int grid = (int)std::min<int64_t>(tiles, sm_count());
+    if (grid < 1) return HS2_ERR_CUDA;
+    auto run = [&](auto kern) {
+        const size_t smem = pgd::Cfg<D, NG>::SMEM;
+        if (!set_smem(kern, smem)) return HS2_ERR_CUDA;
+        kern<<<grid, pgd::kThreads, smem, c.st>>>(
+            mk, mv, static_cast<const __nv_bfloat16*>(c.q), c.ks, c.vs, c.table, work, c.G,
+            s->n_pages, s->max_pages, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.lse,
+            c.part, c.flags);
+        return launch_status();
+    };
+    hs2_status e;
+    switch (s->page) {
+        case 16: e = run(pgd::paged_decode_kernel<D, NG, 16>); break;
+        case 32: e = run(pgd::paged_decode_kernel<D, NG, 32>); break;
+        case 64: e = run(pgd::paged_decode_kernel<D, NG, 64>); break;
+        default: e = run(pgd::paged_decode_kernel<D, NG, 128>);
+    }
+    if (e != HS2_OK) return e;
+    return launch_pdl(pgd::paged_merge_kernel<D>, dim3(s->Hkv, s->B), dim3(D), 0, c.st, work, c.G,
+                      grid, static_cast<__nv_bfloat16*>(c.o), c.lse,
+                      static_cast<const float*>(c.part)) == cudaSuccess
+               ? HS2_OK
+               : HS2_ERR_CUDA;
 }
 
 }  // namespace
@@ -172,7 +246,8 @@ hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_
 
 size_t hs2_paged_decode_workspace(const hs2_paged_shape* shape, int Hq) {
     if (check_paged(shape) != HS2_OK || check_groups(Hq, shape->Hkv) != HS2_OK) return 0;
-    return 16;
+    // two parts of an item per CTA
+    return (size_t)2 * pgd::kMaxCtas * (16 * shape->d + 32) * sizeof(float);
 }
 
 hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, int n_sink,
@@ -192,15 +267,13 @@ hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, in
     unsigned* flags = device_flags();
     if (!flags) return HS2_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto run = [&](auto kern) {
-        kern<<<dim3(Hq, shape->B), 32, 0, st>>>(
-            static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_pages),
-            static_cast<const uint8_t*>(v_pages), k_scale, v_scale, table, lengths,
-            static_cast<__nv_bfloat16*>(o), lse, Hq, shape->Hkv, shape->page, shape->n_pages,
-            shape->max_pages, window, n_sink, scale * kLog2e, flags);
-        return launch_status();
-    };
-    return shape->d == 128 ? run(pgd::paged_rows_kernel<128>) : run(pgd::paged_rows_kernel<64>);
+    const PagedCall c = {shape, q, k_pages, v_pages, k_scale, v_scale, table, lengths,
+                         o,     lse, static_cast<float*>(workspace), Hq / shape->Hkv, window, n_sink,
+                         scale, st, flags};
+    // eight columns a piece where a group has at most eight heads: half the
+    // exponentials and MMA columns of sixteen
+    if (shape->d == 128) return c.G > 8 ? run_paged<128, 16>(c) : run_paged<128, 8>(c);
+    return c.G > 8 ? run_paged<64, 16>(c) : run_paged<64, 8>(c);
 }
 
 hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const void* k,
