@@ -142,7 +142,7 @@ hs2_status run_paged(const PagedCall& c) {
         default: e = run(pgd::paged_decode_kernel<D, NG, 128>);
     }
     if (e != HS2_OK) return e;
-    return launch_pdl(pgd::paged_merge_kernel<D>, dim3(s->Hkv, s->B), dim3(D), 0, c.st, work, c.G,
+    return launch_pdl(pgd::paged_merge_kernel<D>, dim3(s->Hkv * c.G, s->B), dim3(D), 0, c.st, work, c.G,
                       grid, static_cast<__nv_bfloat16*>(c.o), c.lse,
                       static_cast<const float*>(c.part)) == cudaSuccess
                ? HS2_OK

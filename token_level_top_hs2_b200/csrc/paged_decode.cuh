@@ -13,24 +13,32 @@
 //     the error is at most 2^-21 of the largest.
 //   * a weight w (nine significant bits, rounded to nearest) = three e5m2
 //     pieces of 3 bits each, the top bytes of an f16 and of its exact
-//     remainders; what falls below 2^-16 is dropped, with the largest weight
-//     kept between 2^12 and 2^15.
+//     remainders.  e5m2 has no steps below 2^-16: smaller weights round to a
+//     multiple of it, with the largest weight kept between 2^11 and 2^15.
 // The pieces are columns of one MMA (N = 2 or 3 times the heads) and are summed
 // in fp32.  The page's K scale multiplies the logit, its V scale the weight.
 #pragma once
 
+#include "kv_cache.cuh"
 #include "tc.cuh"
 
 namespace hs2 {
 namespace pgd {
 
 using namespace hs2::tc;
+using kvc::e4m3x2;
 
 constexpr int kTile = 128;       // tokens per tile
-constexpr int kThreads = 384;    // producer, QK, PV, Q warps and two softmax groups of four
+constexpr int kThreads = 384;    // K, QK, PV, V warps and two softmax groups of four
 constexpr int kMaxCtas = 148;    // one per SM
-constexpr float kTopLog2 = 12.f;    // a raised reference maps the largest weight to 2^12
+constexpr float kTopLog2 = 11.f;    // a raised reference maps the largest weight to 2^11
+constexpr float kHalfStep = 7.62939453125e-6f;  // 2^-17, half of e5m2's smallest step
 constexpr float kRaiseLog2 = 14.f;  // weights above 2^14 (before the V scale) raise it again
+
+// Scales of pages by their number in the CTA's line of tiles, modulo this: at
+// most 12 stages x 8 pages in flight and two batches of 32 behind them.
+constexpr int kScRing = 256;
+constexpr float kAbsent = -INFINITY;
 
 // A sequence's visible tokens as tiles: those of the first ns tokens, then
 // those of the window [w0, T).
@@ -72,8 +80,10 @@ struct Walk {
         bool bad = false;
         s = span_of(length_of(w.lengths, b, w.cap, &bad), w.window, w.n_sink);
     }
-    HS2_DEV void next(const Work& w, bool more) {
-        if (++t < s.tiles) return;
+    // n tiles on, at most to the item's end; `more`: the line goes on behind them
+    HS2_DEV void skip(const Work& w, int n, bool more) {
+        t += n;
+        if (t < s.tiles) return;
         t = 0;
         if (++h < w.Hkv) return;
         h = 0;
@@ -84,7 +94,6 @@ struct Walk {
         } while (s.tiles == 0 && b + 1 < w.B);
     }
     HS2_DEV int tile() const { return t < s.sink_tiles ? t : s.first + t - s.sink_tiles; }
-    HS2_DEV bool last() const { return t + 1 == s.tiles; }
 };
 
 template <int D, int NG>
@@ -109,11 +118,11 @@ struct Cfg {
 struct Bars {
     uint64_t full[12], empty[12];
     uint64_t s_full[4], s_empty[4];  // [2 * group + buffer]
-    uint64_t p_full[2], p_empty[2];  // [group]
+    uint64_t p_full[2];              // [group]
     uint64_t q_full[2], q_empty[2], x_full, x_empty, drain[2];
-    float2 sc[12][8];       // K and V scale of each page of a stage's tile
-    uint32_t pages[12];     // which of them were there to load
-    float qf[8];            // per item: scale log2(e) over q's power of two
+    float2 sc[kScRing];     // K and V scale of the line's pages, kAbsent for one not loaded
+    int ph[2][2][32];       // per producer and batch: its pages' (page, head) numbers, or -1
+    float qf[12];           // per stage: scale log2(e) over the power of two in q's pieces
     float red[2][4][20];    // per group and warp: per-head maxima or sums, largest V scale
     float xr[16], xl[16];
     unsigned long long total;
@@ -141,6 +150,15 @@ HS2_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The bounded wait of tc.cuh with its slow part out of line: twelve warps run
+// five roles' code here, and what they share of the instruction cache counts.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                       unsigned* flags) {
+    return mbar_wait(bar, parity, abort, flags);
+}
+HS2_DEV bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* flags) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, flags);
+}
 HS2_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Barrier of the 128 threads of a softmax group; true if any of them passes true.
 HS2_DEV bool group_any(int group, bool pred) {
@@ -154,12 +172,67 @@ HS2_DEV bool group_any(int group, bool pred) {
     return r != 0;
 }
 
+// Largest value of a warp's lanes (NaN left out).
+HS2_DEV float warp_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <int N>
 HS2_DEV void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
     if constexpr (N == 32)
         tmem_ld32(taddr, r);
     else
         tmem_ld16(taddr, r);
+}
+
+// One warp splits the G <= NG queries of an item (rows of D bf16) into the
+// rows of their e4m3 pieces, hi in rows 0 .. NG-1 and lo in the next NG, in the
+// K-major layout of the TMA's swizzle.  Returns their power of two.
+template <int D, int NG>
+HS2_DEV float split_q(const __nv_bfloat16* __restrict__ src, int G, uint8_t* dst,
+                      unsigned* flags) {
+    constexpr int PER = NG * D / 8 / 32;  // 16-byte pieces per lane
+    const int lane = lane_id();
+    uint4 x[PER];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < PER; j++) {
+        const int unit = j * 32 + lane;
+        x[j] = unit / (D / 8) < G ? ldg_nc(src + unit * 8) : make_uint4(0, 0, 0, 0);
+        const uint32_t m = __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                                    __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu));
+        top = max(top, max(m & 0xFFFFu, m >> 16));
+    }
+    top = __reduce_max_sync(~0u, top);
+    if (top >= 0x7F80u && lane == 0) atomicOr(flags, FLAG_Q_RANGE);
+    // 2^e max|q| in [128, 256)
+    const int e = min(120, 7 - ((int)(top >> 7) - 127));
+    const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+    for (int j = 0; j < PER; j++) {
+        const int unit = j * 32 + lane, h = unit / (D / 8), c = unit % (D / 8);
+        const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const float a = bf16_lo(in[u]) * f, b = bf16_hi(in[u]) * f;
+            const uint32_t p = e4m3x2(a, b);
+            const float2 r = f16x2_to_float2(e4m3x2_lo_to_f16x2(p));
+            hi[u >> 1] |= p << (16 * (u & 1));
+            lo[u >> 1] |= e4m3x2((a - r.x) * 16.f, (b - r.y) * 16.f) << (16 * (u & 1));
+        }
+        // rows of D bytes, the 16-byte pieces of a row permuted as the
+        // 128-byte (64-byte) swizzle has them
+        auto at = [&](int row) {
+            const uint32_t a = (uint32_t)row * D + c * 8;
+            return a ^ (D == 128 ? (a >> 3) & 0x70u : (a >> 3) & 0x30u);
+        };
+        *reinterpret_cast<uint2*>(dst + at(h)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(dst + at(NG + h)) = make_uint2(lo[0], lo[1]);
+    }
+    return f;
 }
 
 template <int D, int NG, int PAGE>
@@ -185,16 +258,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
 
     if (tid == 0) {
         for (int i = 0; i < NST; i++) {
-            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.full[i], 2);   // the K and the V producer
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 4; i++) {
-            mbar_init(&bars.s_full[i], 2);   // the MMAs, and the issuing thread itself
+            mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.s_empty[i], 4);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.p_empty[i], 1);
             mbar_init(&bars.q_full[i], 1);
             mbar_init(&bars.q_empty[i], 1);
             mbar_init(&bars.drain[i], 1);
@@ -264,193 +336,193 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         w.load(work);
     }
 
-    if (warp == 0) {
-        // ------------------------------------------------------ producer
-        // A lane per page: 32 pages (TPB tiles) at a time, whose numbers and
-        // scales are fetched while the tiles before them are issued.
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------ producers
+        // Warp 0 loads K, warp 3 V (and splits the items' queries: an item's
+        // before its V tiles).  A lane per page: 32 pages (a batch of TPB
+        // tiles) at a time, whose numbers and scales are fetched while the
+        // tiles before them are issued.  One thread issues a batch's copies
+        // from a list in shared memory: an issue takes it about 65 cycles, and
+        // 32 lanes taking turns needed twice as long for a tile.
         constexpr int PP = kTile / PAGE, TPB = 32 / PP;
-        constexpr uint32_t BYTES = PAGE * D;
-        int pid = -1, pos = 0;
+        const int is_v = warp == 3;
+        const float* scale = is_v ? v_scale : k_scale;
+        const CUtensorMap* map = is_v ? &map_v : &map_k;
+        uint8_t* ring = smem + (is_v ? C::OFF_V : 0);
+        Walk mine = w;      // where this lane's page is
+        int pid = -1;
         bool want = false;
-        float ks = 0.f, vs = 0.f;
-        int64_t ph = 0;
-        int hk = 0;
-        auto locate = [&](int i0) {  // this lane's page of tiles i0 .. i0 + TPB - 1
-            want = false;
-            for (int s = 0; s < TPB && i0 + s < n_tiles; s++) {
-                if (lane / PP == s) {
-                    const int p = w.tile() * PP + lane % PP;
-                    pos = p * PAGE;
-                    want = pos < w.s.T && (pos + PAGE > w.s.w0 || pos < w.s.ns);
-                    pid = want ? __ldg(table + (size_t)w.b * max_pages + p) : -1;
-                    hk = w.h;
-                }
-                w.next(work, i0 + s + 1 < n_tiles);
+        float sc = 0.f;
+        int ph = -1;
+        // this lane's page of the tiles i0 .. i0 + TPB - 1, and its number
+        auto locate = [&](int i0) {
+            mine = w;
+            int left = min(lane / PP, n_tiles - 1 - i0);  // tiles on from i0's
+            while (left > 0 && mine.t + left >= mine.s.tiles) {
+                const int n = mine.s.tiles - mine.t;
+                left -= n;
+                mine.skip(work, n, true);
             }
+            mine.t += max(left, 0);
+            const int p = mine.tile() * PP + lane % PP, pos = p * PAGE;
+            want = i0 + lane / PP < n_tiles && pos < mine.s.T &&
+                   (pos + PAGE > mine.s.w0 || pos < mine.s.ns);
+            pid = want ? __ldg(table + (size_t)mine.b * max_pages + p) : -1;
+        };
+        // the first tile of the batch behind: one on from lane 31's
+        auto move_on = [&](int i0) {
+            if (i0 + TPB >= n_tiles) return;
+            w.b = __shfl_sync(~0u, mine.b, 31);
+            w.h = __shfl_sync(~0u, mine.h, 31);
+            w.t = __shfl_sync(~0u, mine.t, 31);
+            w.load(work);
+            w.skip(work, 1, true);
         };
         auto scales = [&]() {
             if (want && (pid < 0 || pid >= n_pages)) {
                 atomicOr(flags, FLAG_BAD_INDEX);
                 want = false;
             }
-            ph = (int64_t)pid * Hkv + hk;
-            ks = want ? __ldg(k_scale + ph) : 0.f;
-            vs = want ? __ldg(v_scale + ph) : 0.f;
+            ph = want ? pid * Hkv + mine.h : -1;
+            sc = want ? __ldg(scale + ph) : kAbsent;
         };
-        int armed = 0;
+        int armed = 0, seg = 0, st = 0;
+        uint32_t ring_phase = 1;  // of the empty barriers: the first round passes
+        float qf = 0.f;
         bool ok = true;
         locate(0);
         scales();
-        for (int i0 = 0; ok && i0 < n_tiles; i0 += TPB) {
-            const bool want_c = want;
-            const float ks_c = ks, vs_c = vs;
-            const int ph_c = (int)ph;
-            for (int s = 0; s < TPB && i0 + s < n_tiles; s++) {
-                const int i = i0 + s, st = i % NST;
-                if (i >= NST)
-                    ok = __all_sync(~0u, mbar_wait(&bars.empty[st], (i / NST - 1) & 1, abort_, flags));
-                if (!ok) break;
-                const bool mine = lane / PP == s, load = mine && want_c;
-                if (mine) bars.sc[st][lane % PP] = make_float2(ks_c, vs_c);
-                const uint32_t mask = __ballot_sync(~0u, load) >> (s * PP);
-                if (lane == 0) bars.pages[st] = mask;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&bars.full[st],
-                                          2 * BYTES * __popc(mask & ((1u << PP) - 1)));
-                __syncwarp();
-                if (load) {
-                    const int row = (lane % PP) * PAGE;
-                    tma_load_3d(smem + st * C::KV + row * D, &map_k, 0, 0, ph_c, &bars.full[st]);
-                    tma_load_3d(smem + C::OFF_V + st * C::KV + row * D, &map_v, 0, 0, ph_c,
-                                &bars.full[st]);
+        for (int i0 = 0, buf = 0; ok && i0 < n_tiles; i0 += TPB, buf ^= 1) {
+            const int cnt = min(TPB, n_tiles - i0);
+            // the batch's list, and which of its tiles open an item
+            bars.ph[is_v][buf][lane] = ph;
+            float2* to = &bars.sc[(i0 * PP + lane) & (kScRing - 1)];
+            if (is_v)
+                to->y = sc;
+            else
+                to->x = sc;
+            const int b_c = mine.b, h_c = mine.h;
+            const uint32_t opens = __ballot_sync(
+                ~0u, lane % PP == 0 && lane / PP < cnt && (mine.t == 0 || (i0 == 0 && lane == 0)));
+            move_on(i0);
+            locate(i0 + TPB);  // (their numbers arrive during the first half)
+            for (int s = 0; ok && s < cnt;) {
+                if (is_v && (opens >> (s * PP) & 1)) {
+                    const int b = __shfl_sync(~0u, b_c, s * PP), h = __shfl_sync(~0u, h_c, s * PP);
+                    ok = __all_sync(~0u, wait(&bars.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_,
+                                                   flags));
+                    if (!ok) break;
+                    qf = scale2 / split_q<D, NG>(q + ((size_t)b * Hkv + h) * G * D, G,
+                                                 smem + C::OFF_Q + (seg & 1) * C::QB, flags);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.q_full[seg & 1]);
+                    seg++;
                 }
-                armed++;
-                if (s == 0) locate(i0 + TPB);
-                if (s == TPB / 2) scales();
+                int e = s < TPB / 2 ? min(cnt, TPB / 2) : cnt;
+                if (is_v) {
+                    const uint32_t next = opens & ~((2u << (s * PP)) - 1);  // (s * PP < 32)
+                    if (next) e = min(e, (__ffs(next) - 1) / PP);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    for (int j = s; j < e; j++) {
+                        int phs[PP], n = 0;
+#pragma unroll
+                        for (int u = 0; u < PP; u++) phs[u] = bars.ph[is_v][buf][j * PP + u];
+#pragma unroll
+                        for (int u = 0; u < PP; u++) n += phs[u] >= 0;
+                        ok = wait(&bars.empty[st], ring_phase, abort_, flags);
+                        if (!ok) break;
+                        if (is_v) bars.qf[st] = qf;
+                        mbar_arrive_expect_tx(&bars.full[st], PAGE * D * n);
+#pragma unroll
+                        for (int u = 0; u < PP; u++)
+                            if (phs[u] >= 0)
+                                tma_load_3d(ring + st * C::KV + u * PAGE * D, map, 0, 0, phs[u],
+                                            &bars.full[st]);
+                        armed++;
+                        if (++st == NST) st = 0, ring_phase ^= 1;
+                    }
+                }
+                ok = __shfl_sync(~0u, ok, 0);
+                if (s < TPB / 2 && e >= min(cnt, TPB / 2)) scales();
+                s = e;
             }
         }
-        if (*abort_) {  // let the copies still in flight land before the CTA leaves
+        if (*abort_ && lane == 0) {  // let the copies in flight land before the CTA leaves
+            // (the other producer's share of a barrier may never come: the wait
+            // is bounded, and by its end the copies have landed)
             volatile int no_abort = 0;
             for (int i = max(0, armed - NST); i < armed; i++)
-                mbar_wait(&bars.full[i % NST], (i / NST) & 1, &no_abort, flags);
+                wait(&bars.full[i % NST], (i / NST) & 1, &no_abort, flags);
         }
     } else if (warp == 1) {
         // ------------------------------------------------- S^T = K q^T
         constexpr uint32_t id = idesc_f8(C::NQ, 0, false, false);
         if (lane == 0 && n_tiles > 0) {
-            bool fresh = true;
-            int seg = 0;
-            for (int i = 0; i < n_tiles; i++) {
-                const int st = i % NST, sb = (i & 1) * 2 + ((i >> 1) & 1);
-                if (fresh && !mbar_wait(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags)) break;
-                if (!mbar_wait(&bars.full[st], (i / NST) & 1, abort_, flags)) break;
-                if (i >= 4 && !mbar_wait(&bars.s_empty[sb], ((i >> 2) - 1) & 1, abort_, flags)) break;
-                fence_after_sync();
-                const uint32_t a = smem_u32(smem + st * C::KV);
-                const uint32_t bq = smem_u32(smem + C::OFF_Q + (seg & 1) * C::QB);
+            const uint64_t a0 = sdesc(SWZ, smem_u32(smem), 16, ATOM);
+            const uint64_t q0 = sdesc(SWZ, smem_u32(smem + C::OFF_Q), 16, ATOM);
+            int st = 0, seg = 0;
+            uint32_t ring_phase = 0;
+            bool ok = true;
+            for (int i = 0; ok && i < n_tiles; seg++) {
+                const int n = min(w.s.tiles - w.t, n_tiles - i);
+                ok = wait(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags);
+                for (const int end = i + n; ok && i < end; i++) {
+                    const int sb = (i & 1) * 2 + ((i >> 1) & 1);
+                    if (!wait(&bars.full[st], ring_phase, abort_, flags) ||
+                        !wait(&bars.s_empty[sb], ((i >> 2) & 1) ^ 1, abort_, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint64_t a = a0 + ((st * C::KV) >> 4), bq = q0 + (((seg & 1) * C::QB) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ks++)
-                    mma_f8(tmem + sb * 32, sdesc(SWZ, a + ks * 32, 16, ATOM),
-                           sdesc(SWZ, bq + ks * 32, 16, ATOM), id, ks > 0);
-                mma_commit(&bars.s_full[sb]);
-                fresh = w.last();
-                if (fresh) mma_commit(&bars.q_empty[seg++ & 1]);
-                mbar_arrive(&bars.s_full[sb]);
-                w.next(work, i + 1 < n_tiles);
+                    for (int ks = 0; ks < D / 32; ks++)
+                        mma_f8(tmem + sb * 32, a + ks * 2, bq + ks * 2, id, ks > 0);
+                    mma_commit(&bars.s_full[sb]);
+                    if (i + 1 == end) mma_commit(&bars.q_empty[seg & 1]);
+                    if (++st == NST) st = 0, ring_phase ^= 1;
+                }
+                w.skip(work, n, i < n_tiles);
             }
             mma_commit(&bars.drain[0]);
             volatile int no_abort = 0;
-            mbar_wait(&bars.drain[0], 0, &no_abort, flags);
+            wait(&bars.drain[0], 0, &no_abort, flags);
         }
     } else if (warp == 2) {
         // ----------------------------------------------- O^T += V^T w^T
         constexpr uint32_t id = idesc_f8(C::NP, 1, true, true);
         if (lane == 0 && n_tiles > 0) {
-            bool acc[2] = {false, false};
-            for (int i = 0; i < n_tiles; i++) {
-                const int st = i % NST, g = i & 1;
-                if (!mbar_wait(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) break;
-                fence_after_sync();
-                const uint32_t a = smem_u32(smem + C::OFF_V + st * C::KV);
-                const uint32_t bp = smem_u32(smem + C::OFF_P + g * C::PB);
+            // V: dims contiguous, eight tokens per atom; 64 dims are read twice
+            // (a zero step between 64-dim blocks) for the 128 rows
+            const uint64_t a0 = sdesc(SWZ, smem_u32(smem + C::OFF_V), 0, ATOM);
+            const uint64_t p0 = sdesc(0, smem_u32(smem + C::OFF_P), 128, kTile * 16);
+            int st = 0;
+            bool ok = true;
+            for (int i = 0; ok && i < n_tiles;) {
+                const int n = min(w.s.tiles - w.t, n_tiles - i);
+                for (int j = 0; j < n; j++, i++) {
+                    const int g = i & 1;
+                    if (!wait(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint64_t a = a0 + ((st * C::KV) >> 4), bp = p0 + ((g * C::PB) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 32; ks++)
-                    // V: dims contiguous, eight tokens per atom; 64 dims are read twice
-                    // (a zero step between 64-dim blocks) for the 128 rows
-                    mma_f8(tmem + C::COL_O + g * 64, sdesc(SWZ, a + ks * 32 * D, 0, ATOM),
-                           sdesc(0, bp + ks * 512, 128, kTile * 16), id,
-                           (acc[g] || ks > 0) ? 1u : 0u);
-                mma_commit(&bars.empty[st]);
-                mma_commit(&bars.p_empty[g]);
-                acc[g] = true;
-                if (w.last()) acc[0] = acc[1] = false;
-                w.next(work, i + 1 < n_tiles);
+                    for (int ks = 0; ks < kTile / 32; ks++)
+                        mma_f8(tmem + C::COL_O + g * 64, a + ((ks * 32 * D) >> 4),
+                               bp + ((ks * 512) >> 4), id, (j > 1 || ks > 0) ? 1u : 0u);
+                    mma_commit(&bars.empty[st]);
+                    if (++st == NST) st = 0;
+                }
+                w.skip(work, n, i < n_tiles);
             }
             mma_commit(&bars.drain[1]);
             volatile int no_abort = 0;
-            mbar_wait(&bars.drain[1], 0, &no_abort, flags);
-        }
-    } else if (warp == 3) {
-        // --------------------------------------------------- q's pieces
-        int seg = 0;
-        for (int i = 0; i < n_tiles; seg++) {
-            if (seg >= 2 &&
-                !__all_sync(~0u, mbar_wait(&bars.q_empty[seg & 1], ((seg >> 1) - 1) & 1, abort_, flags)))
-                break;
-            uint8_t* dst = smem + C::OFF_Q + (seg & 1) * C::QB;
-            const __nv_bfloat16* src = q + ((size_t)w.b * Hkv + w.h) * G * D;
-            constexpr int PER = NG * D / 8 / 32;  // 16-byte pieces per lane
-            uint4 x[PER];
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < PER; j++) {
-                const int unit = j * 32 + lane;
-                x[j] = unit / (D / 8) < G ? ldg_nc(src + unit * 8) : make_uint4(0, 0, 0, 0);
-                const uint32_t m = __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
-                                            __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu));
-                top = max(top, max(m & 0xFFFFu, m >> 16));
-            }
-            top = __reduce_max_sync(~0u, top);
-            if (top >= 0x7F80u && lane == 0) atomicOr(flags, FLAG_Q_RANGE);
-            // 2^e max|q| in [128, 256)
-            const int e = min(120, 7 - ((int)(top >> 7) - 127));
-            const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll
-            for (int j = 0; j < PER; j++) {
-                const int unit = j * 32 + lane, h = unit / (D / 8), c = unit % (D / 8);
-                const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-                for (int u = 0; u < 4; u++) {
-                    const float a = bf16_lo(in[u]) * f, b = bf16_hi(in[u]) * f;
-                    uint16_t ph_, pl_;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ph_) : "f"(b), "f"(a));
-                    const float2 r = f16x2_to_float2(e4m3x2_lo_to_f16x2(ph_));
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                        : "=h"(pl_)
-                        : "f"((b - r.y) * 16.f), "f"((a - r.x) * 16.f));
-                    hi[u >> 1] |= (uint32_t)ph_ << (16 * (u & 1));
-                    lo[u >> 1] |= (uint32_t)pl_ << (16 * (u & 1));
-                }
-                // rows of D bytes, the 16-byte pieces of a row permuted as the
-                // 128-byte (64-byte) swizzle has them
-                auto at = [&](int row) {
-                    const uint32_t a = (uint32_t)row * D + c * 8;
-                    return a ^ (D == 128 ? (a >> 3) & 0x70u : (a >> 3) & 0x30u);
-                };
-                *reinterpret_cast<uint2*>(dst + at(h)) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(dst + at(NG + h)) = make_uint2(lo[0], lo[1]);
-            }
-            if (lane == 0) bars.qf[seg & 7] = scale2 / f;
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.q_full[seg & 1]);
-            // on to the next item
-            const int left = w.s.tiles - w.t;
-            i += left;
-            w.t = w.s.tiles - 1;
-            w.next(work, i < n_tiles);
+            wait(&bars.drain[1], 0, &no_abort, flags);
         }
     } else {
         // ------------------------------------------------------ softmax
@@ -462,25 +534,31 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + g * 64;
         float R[NG], l[NG], vref = 0.f, vinv = 0.f;
-        int own = 0, other = 0;    // tiles of the segment that each group takes
-        int seg = 0, n_x = 0;      // segments and hand-overs so far
-        bool at_start = true;        // the segment begins where the CTA does
-        bool from_top = w.t == 0;    // the segment begins where its item does
-        bool has = false, ok = true;  // R and vref are set
+        int n_x = 0;                  // hand-overs so far
+        int st = g, st_was = 0;       // stages of the group's tile and of its last one
+        uint32_t ph = 0, ph_was = 0;  // and their barriers' phases
+        bool at_start = true;         // the segment begins where the CTA does
+        bool from_top = w.t == 0;     // the segment begins where its item does
+        bool has = false, ok = true;  // R and vref are set; no wait has given up
 #pragma unroll
         for (int h = 0; h < NG; h++) R[h] = 0.f, l[h] = 0.f;
 
-        for (int i = 0; i < n_tiles; i++) {
-            if ((i & 1) == g) {
-                const int k = i >> 1, st = i % NST, sb = g * 2 + (k & 1);
-                ok = ok && mbar_wait(&bars.s_full[sb], (k >> 1) & 1, abort_, flags);
-                fence_after_sync();
-                const int s = w.tile() * kTile + row;
-                const float2 sc = bars.sc[st][row / PAGE];
-                const bool vis = s < w.s.T && (s >= w.s.w0 || s < w.s.ns) &&
-                                 ((bars.pages[st] >> (row / PAGE)) & 1);
-                const float f = vis ? sc.x * bars.qf[seg & 7] : 0.f;
+        for (int i0 = 0; i0 < n_tiles;) {
+            const int n = min(w.s.tiles - w.t, n_tiles - i0);  // tiles of the segment
+            const int mine = (n + 1 - ((i0 ^ g) & 1)) / 2, others = n - mine;
+            int j = (i0 ^ g) & 1;
+            for (; j < n; j += 2) {
+                const int k = (i0 + j) >> 1, sb = g * 2 + (k & 1);
+                const int t = w.t + j;
+                const int s = (t < w.s.sink_tiles ? t : w.s.first + t - w.s.sink_tiles) * kTile + row;
+                // the tile's copies have landed: its scales are there
+                ok = ok && wait(&bars.full[st], ph, abort_, flags);
+                const float2 sc = bars.sc[((i0 + j) * (kTile / PAGE) + row / PAGE) & (kScRing - 1)];
+                const bool vis = s < w.s.T && (s >= w.s.w0 || s < w.s.ns) && sc.x != kAbsent;
+                const float f = vis ? sc.x * bars.qf[st] : 0.f;
                 const float sv = vis ? sc.y : 0.f;
+                ok = ok && wait(&bars.s_full[sb], (k >> 1) & 1, abort_, flags);
+                fence_after_sync();
                 uint32_t r[C::NQ];
                 tmem_ldn<C::NQ>(lanes + sb * 32, r);
                 tmem_ld_wait();
@@ -497,17 +575,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 const bool raise = vis && (!has || top > kRaiseLog2 || sv > 2.f * vref);
                 if (group_any(g, raise || !ok)) {
                     // a new reference (the segment's first tile, or a larger weight)
-                    if (ok && own > 0)
-                        ok = mbar_wait(&bars.p_empty[g], (k - 1) & 1, abort_, flags);
+                    if (j > 1) ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
                     fence_after_sync();
 #pragma unroll
                     for (int h = 0; h < NG; h++) {
                         float x = vis ? y[h] + R[h] : -INFINITY;
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+                        x = warp_max(x);
                         if (lane == 0) bars.red[g][wq][h] = x;
                     }
                     const float sm = __uint_as_float(
@@ -536,8 +609,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                         l[h] *= a[h];
                     }
                     has = true;
-                    if (own > 0) {
-#pragma unroll
+                    if (j > 1) {
+#pragma unroll 1
                         for (int c = 0; c < C::NP; c += 16) {
                             uint32_t v[16];
                             tmem_ld16(o_col + c, v);
@@ -545,7 +618,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                             for (int u = 0; u < 16; u++)
                                 v[u] = __float_as_uint(__uint_as_float(v[u]) *
-                                                       (a[(c + u) % NG] * beta));
+                                                       (a[u % NG] * beta));
                             tmem_st16(o_col + c, v);
                         }
                         tmem_st_wait();
@@ -560,8 +633,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     const float p0 = vis ? ex2(y[h]) : 0.f, p1 = vis ? ex2(y[h + 1]) : 0.f;
                     l[h] += p0;
                     l[h + 1] += p1;
-                    // nine significant bits: half a step added, the last two bits cut
-                    pc[h / 2] = (pack_f16(p0 * rv, p1 * rv) + 0x00020002u) & 0xFFFCFFFCu;
+                    // nine significant bits, and no step below 2^-16: half a step of
+                    // each added, what is below it cut
+                    pc[h / 2] = (pack_f16(fmaf(p0, rv, kHalfStep), fmaf(p1, rv, kHalfStep)) + 0x00020002u) &
+                                0xFFFCFFFCu;
                 }
                 uint32_t b1[NG / 4], b2[NG / 4], b3[NG / 4];
 #pragma unroll
@@ -579,7 +654,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     x0 = rest(x0), x1 = rest(x1);
                     b3[j] = prmt(x0, x1, 0x7531u);
                 }
-                if (k > 0) ok = ok && mbar_wait(&bars.p_empty[g], (k - 1) & 1, abort_, flags);
+                if (k > 0) ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
                 uint8_t* p = smem + C::OFF_P + g * C::PB + row * 16;
                 if constexpr (NG == 16) {
                     *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
@@ -591,7 +666,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 }
                 if (!vis) {
                     // 0 * NaN is NaN: a row that is not visible must not hold one
-                    ok = ok && mbar_wait(&bars.full[st], (i / NST) & 1, abort_, flags);
                     uint4* v = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::KV + row * D);
                     if (ok)
 #pragma unroll
@@ -600,115 +674,121 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[g]);
+                st_was = st, ph_was = ph;
+                st += 2;
+                if (st >= NST) st -= NST, ph ^= 1;
             }
-            own += (i & 1) == g;
-            other += (i & 1) != g;
-            const bool item_end = w.last();
-            if (item_end || i + 1 == n_tiles) {
+            if (j < n) break;  // the group has given up
+            const bool item_end = w.t + n == w.s.tiles;
+            if (mine > 0) {
                 // ------------------------------------ the segment's result
-                if (own > 0) {
-                    const int k = (i - ((i & 1) != g)) >> 1;  // the group's last tile
-                    ok = ok && mbar_wait(&bars.p_empty[g], k & 1, abort_, flags);
-                    fence_after_sync();
+                ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
+                fence_after_sync();
+                // sums over the warp's lanes: each step halves the heads a lane holds
 #pragma unroll
-                    for (int h = 0; h < NG; h++) {
-                        float x = l[h];
+                for (int c = NG / 2, off = 16; off > 0; c /= 2, off /= 2) {
+                    const bool up = lane & off;
+                    if (c == 0) {
+                        l[0] += __shfl_xor_sync(~0u, l[0], off);
+                    } else {
 #pragma unroll
-                        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
-                        if (lane == 0) bars.red[g][wq][h] = x;
+                        for (int h = 0; h < c; h++) {
+                            const float give = up ? l[h] : l[h + c];
+                            l[h] = (up ? l[h + c] : l[h]) + __shfl_xor_sync(~0u, give, off);
+                        }
                     }
-                    if (group_any(g, !ok)) {
-                        ok = false;
-                        break;
+                }
+                if (lane % (32 / NG) == 0) bars.red[g][wq][lane / (32 / NG)] = l[0];
+                if (group_any(g, !ok)) {
+                    ok = false;
+                    break;
+                }
+                float O[NG];
+                {
+                    uint32_t v[16];
+                    tmem_ld16(o_col, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int h = 0; h < NG; h++) O[h] = __uint_as_float(v[h]);
+                    if constexpr (NG == 8) {
+#pragma unroll
+                        for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[8 + h]);
                     }
-                    float O[NG];
-                    {
-                        uint32_t v[16];
-                        tmem_ld16(o_col, v);
+#pragma unroll
+                    for (int c = 16; c < C::NP; c += 16) {
+                        tmem_ld16(o_col + c, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int h = 0; h < NG; h++) O[h] = __uint_as_float(v[h]);
-                        if constexpr (NG == 8) {
-#pragma unroll
-                            for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[8 + h]);
-                        }
-#pragma unroll
-                        for (int c = 16; c < C::NP; c += 16) {
-                            tmem_ld16(o_col + c, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[h]);
-                        }
+                        for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[h]);
                     }
-                    fence_before_sync();
-#pragma unroll
-                    for (int h = 0; h < NG; h++) {
-                        O[h] *= vref;
-                        l[h] = 0.f;
-#pragma unroll
-                        for (int u = 0; u < 4; u++) l[h] += bars.red[g][u][h];
-                        if (!has) R[h] = -1e30f;  // nothing visible: no weight when merged
-                    }
-                    float* xo = reinterpret_cast<float*>(smem + C::OFF_X);
-                    const bool both = other > 0;
-                    if (both && g == 1) {
-                        // hand the result to group 0
-                        if (n_x > 0)
-                            ok = ok && mbar_wait(&bars.x_empty, (n_x - 1) & 1, abort_, flags);
-                        if (row < D)
-#pragma unroll
-                            for (int h = 0; h < NG; h++) xo[h * D + row] = O[h];
-                        if (row == 0)
-#pragma unroll
-                            for (int h = 0; h < NG; h++) bars.xr[h] = R[h], bars.xl[h] = l[h];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.x_full);
-                    } else {
-                        if (both) {
-                            ok = ok && mbar_wait(&bars.x_full, n_x & 1, abort_, flags);
-#pragma unroll
-                            for (int h = 0; h < NG; h++) {
-                                const float xr = bars.xr[h], M = fmaxf(R[h], xr);
-                                const float a = ex2(R[h] - M), b = ex2(xr - M);
-                                O[h] = O[h] * a + (row < D ? xo[h * D + row] : 0.f) * b;
-                                l[h] = l[h] * a + bars.xl[h] * b;
-                                R[h] = M;
-                            }
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars.x_empty);
-                        }
-                        const size_t q0 = ((size_t)w.b * Hkv + w.h) * G;
-                        if (ok && from_top && item_end) {
-#pragma unroll
-                            for (int h = 0; h < NG; h++) {
-                                if (h >= G) break;
-                                const bool any = l[h] != 0.f;
-                                if (row < D)
-                                    o[(q0 + h) * D + row] = __float2bfloat16(any ? O[h] / l[h] : 0.f);
-                                if (lse && row == h)
-                                    lse[q0 + h] = any ? (R[h] + log2f(l[h])) * kLn2 : -INFINITY;
-                            }
-                        } else if (ok) {
-                            float* ps = part + (size_t)(2 * cta + (at_start ? 0 : 1)) * C::PART;
-#pragma unroll
-                            for (int h = 0; h < NG; h++) {
-                                if (row < D) ps[h * D + row] = O[h];
-                                if (row == h) ps[16 * D + h] = R[h], ps[16 * D + 16 + h] = l[h];
-                            }
-                        }
-                    }
-                    if (both) n_x++;
-#pragma unroll
-                    for (int h = 0; h < NG; h++) R[h] = 0.f, l[h] = 0.f;
-                    vref = vinv = 0.f;
-                    has = false;
                 }
-                own = other = 0;
-                seg++;
-                at_start = false;
-                from_top = true;
-            }
-            w.next(work, i + 1 < n_tiles);
+                fence_before_sync();
+#pragma unroll
+                for (int h = 0; h < NG; h++) {
+                    O[h] *= vref;
+                    l[h] = 0.f;
+#pragma unroll
+                    for (int u = 0; u < 4; u++) l[h] += bars.red[g][u][h];
+                    if (!has) R[h] = -1e30f;  // nothing visible: no weight when merged
+                }
+                float* xo = reinterpret_cast<float*>(smem + C::OFF_X);
+                const bool both = others > 0;
+                if (both && g == 1) {
+                    // hand the result to group 0
+                    if (n_x > 0)
+                        ok = ok && wait(&bars.x_empty, (n_x - 1) & 1, abort_, flags);
+                    if (row < D)
+#pragma unroll
+                        for (int h = 0; h < NG; h++) xo[h * D + row] = O[h];
+                    if (row == 0)
+#pragma unroll
+                        for (int h = 0; h < NG; h++) bars.xr[h] = R[h], bars.xl[h] = l[h];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.x_full);
+                } else {
+                    if (both) {
+                        ok = ok && wait(&bars.x_full, n_x & 1, abort_, flags);
+#pragma unroll
+                        for (int h = 0; h < NG; h++) {
+                            const float xr = bars.xr[h], M = fmaxf(R[h], xr);
+                            const float a = ex2(R[h] - M), b = ex2(xr - M);
+                            O[h] = O[h] * a + (row < D ? xo[h * D + row] : 0.f) * b;
+                            l[h] = l[h] * a + bars.xl[h] * b;
+                            R[h] = M;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.x_empty);
+                    }
+                    const size_t q0 = ((size_t)w.b * Hkv + w.h) * G;
+                    if (ok && from_top && item_end) {
+#pragma unroll
+                        for (int h = 0; h < NG; h++) {
+                            if (h >= G) break;
+                            const bool any = l[h] != 0.f;
+                            if (row < D)
+                                o[(q0 + h) * D + row] = __float2bfloat16(any ? O[h] / l[h] : 0.f);
+                            if (lse && row == h)
+                                lse[q0 + h] = any ? (R[h] + log2f(l[h])) * kLn2 : -INFINITY;
+                        }
+                    } else if (ok) {
+                        float* ps = part + (size_t)(2 * cta + (at_start ? 0 : 1)) * C::PART;
+#pragma unroll
+                        for (int h = 0; h < NG; h++) {
+                            if (row < D) ps[h * D + row] = O[h];
+                            if (row == h) ps[16 * D + h] = R[h], ps[16 * D + 16 + h] = l[h];
+                        }
+                    }
+                }
+                if (both) n_x++;
+#pragma unroll
+                for (int h = 0; h < NG; h++) R[h] = 0.f, l[h] = 0.f;
+                vref = vinv = 0.f;
+                has = false;
+                }
+            at_start = false;
+            from_top = true;
+            i0 += n;
+            w.skip(work, n, i0 < n_tiles);
         }
     }
     fence_before_sync();
@@ -720,14 +800,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
 }
 
 // Items cut between CTAs: their parts in the order of the line.  Sequences
-// without visible tokens get zeros.  grid (Hkv, B), a thread per dim.
+// without visible tokens get zeros.  grid (Hq, B), a thread per dim; the parts'
+// references and sums are read by a lane each, their outputs eight at a time.
 template <int D>
 __global__ void __launch_bounds__(D)
 paged_merge_kernel(const Work work, int G, int n_grid, __nv_bfloat16* __restrict__ o,
                    float* __restrict__ lse, const float* __restrict__ part) {
     constexpr int PART = 16 * D + 32;
     __shared__ unsigned long long s_before, s_total;
-    const int tid = threadIdx.x, hk = blockIdx.x, b = blockIdx.y;
+    __shared__ float s_a[kMaxCtas];
+    const int tid = threadIdx.x, hk = blockIdx.x / G, h = blockIdx.x % G, b = blockIdx.y;
     if (tid == 0) s_before = s_total = 0;
     __syncthreads();
     unsigned long long before = 0, total = 0;
@@ -742,36 +824,46 @@ paged_merge_kernel(const Work work, int G, int n_grid, __nv_bfloat16* __restrict
     __syncthreads();
     const int64_t all = (int64_t)s_total * work.Hkv;
     const int nt = span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
-    const size_t q0 = ((size_t)b * work.Hkv + hk) * G;
+    const size_t row = ((size_t)b * work.Hkv + hk) * G + h;
     griddep_wait();
     if (nt == 0) {
-        for (int h = 0; h < G; h++) {
-            o[(q0 + h) * D + tid] = __float2bfloat16(0.f);
-            if (lse && tid == h) lse[q0 + h] = -INFINITY;
-        }
+        o[row * D + tid] = __float2bfloat16(0.f);
+        if (lse && tid == 0) lse[row] = -INFINITY;
         return;
     }
     const int n = (int)min((int64_t)n_grid, all);
     const int64_t t0 = (int64_t)s_before * work.Hkv + (int64_t)hk * nt, t1 = t0 + nt;
     auto owner = [&](int64_t t) { return (int)(((t + 1) * n + all - 1) / all) - 1; };
-    const int c0 = owner(t0), c1 = owner(t1 - 1);
-    if (c0 == c1) return;
+    const int c0 = owner(t0), c1 = owner(t1 - 1), np = c1 - c0 + 1;
+    if (np == 1) return;
     const int first = 2 * c0 + (cut(all, c0, n) == t0 ? 0 : 1);
-    for (int h = 0; h < G; h++) {
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; c++)
-            M = fmaxf(M, part[(size_t)(c == c0 ? first : 2 * c) * PART + 16 * D + h]);
-        float O = 0.f, l = 0.f;
-        for (int c = c0; c <= c1; c++) {
-            const float* p = part + (size_t)(c == c0 ? first : 2 * c) * PART;
-            const float a = ex2(p[16 * D + h] - M);
-            O = fmaf(a, p[h * D + tid], O);
-            l = fmaf(a, p[16 * D + 16 + h], l);
-        }
-        const bool any = l != 0.f;
-        o[(q0 + h) * D + tid] = __float2bfloat16(any ? O / l : 0.f);
-        if (lse && tid == h) lse[q0 + h] = any ? (M + log2f(l)) * kLn2 : -INFINITY;
+    auto at = [&](int i) { return part + (size_t)(i == 0 ? first : 2 * (c0 + i)) * PART; };
+    // every warp finds the common reference and the sum
+    float M = -INFINITY, l = 0.f;
+    for (int i = tid & 31; i < np; i += 32) M = fmaxf(M, at(i)[16 * D + h]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
+    for (int i = tid & 31; i < np; i += 32) {
+        const float* p = at(i) + 16 * D;
+        const float a = ex2(p[h] - M);
+        if (tid < 32) s_a[i] = a;
+        l = fmaf(a, p[16 + h], l);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(~0u, l, off);
+    __syncthreads();
+    float O = 0.f;
+    for (int i0 = 0; i0 < np; i0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = i0 + j < np ? at(i0 + j)[h * D + tid] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (i0 + j < np) O = fmaf(s_a[i0 + j], v[j], O);
+    }
+    const bool any = l != 0.f;
+    o[row * D + tid] = __float2bfloat16(any ? O / l : 0.f);
+    if (lse && tid == 0) lse[row] = any ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace pgd
