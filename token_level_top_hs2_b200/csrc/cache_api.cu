@@ -149,6 +149,35 @@ hs2_status run_paged(const PagedCall& c) {
                : HS2_ERR_CUDA;
 }
 
+// [B, L, H, D] bf16: a box of 64 columns, `heads` heads and `rows` positions.
+bool map_rows(CUtensorMap* m, const void* x, int B, int L, int H, int D, int heads, int rows) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)L, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2,
+                                   (cuuint64_t)L * H * D * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
+    return map_bf16(m, x, 4, dims, strides, box);
+}
+
+template <int D>
+hs2_status run_window(const win::Shape& s, const void* q, const void* k, const void* v, void* o,
+                      float* lse, cudaStream_t st, unsigned* flags) {
+    win::Maps m;
+    if (!map_rows(&m.q, q, s.B, s.Lq, s.Hq, D, s.G, s.nt) ||
+        !map_rows(&m.o, o, s.B, s.Lq, s.Hq, D, s.G, s.nt) ||
+        !map_rows(&m.k64, k, s.B, s.Lk, s.Hkv, D, 1, win::BN) ||
+        !map_rows(&m.k16, k, s.B, s.Lk, s.Hkv, D, 1, 16) ||
+        !map_rows(&m.v64, v, s.B, s.Lk, s.Hkv, D, 1, win::BN) ||
+        !map_rows(&m.v16, v, s.B, s.Lk, s.Hkv, D, 1, 16))
+        return HS2_ERR_CUDA;
+    const int grid = std::min(s.items, sm_count());
+    const size_t smem = win::Cfg<D>::SMEM;
+    if (grid < 1 || !set_smem(win::window_attn_kernel<D>, smem)) return HS2_ERR_CUDA;
+    win::window_attn_kernel<D><<<grid, win::kThreads, smem, st>>>(
+        m, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+        static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse, s, flags);
+    return launch_status();
+}
+
 }  // namespace
 
 extern "C" {
@@ -288,16 +317,15 @@ hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const v
     if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
     if (!pointers_ok(q, k, v, o) || !aligned16(lse)) return HS2_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t blocks = ((int64_t)s->B * s->Lq * s->Hq + 3) / 4;
-    if (blocks > INT_MAX) return HS2_ERR_UNSUPPORTED;
-    auto run = [&](auto kern) {
-        kern<<<(unsigned)blocks, 128, 0, st>>>(
-            static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-            static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse, s->B, s->Lq,
-            s->Lk, s->Hq, s->Hkv, s->window, s->n_sink, s->scale * kLog2e);
-        return launch_status();
-    };
-    return s->d == 128 ? run(win::window_rows_kernel<128>) : run(win::window_rows_kernel<64>);
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
+    const int G = s->Hq / s->Hkv, nt = win::BM / G;
+    const int64_t blocks = ((int64_t)s->Lq + 2 * nt - 1) / (2 * nt);
+    if (blocks * s->B * s->Hkv > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    const win::Shape sh = {s->B, s->Lq, s->Lk, s->Hq, s->Hkv, G, nt, s->window, s->n_sink, (int)blocks,
+                           (int)(blocks * s->B * s->Hkv), s->scale * kLog2e};
+    return s->d == 128 ? run_window<128>(sh, q, k, v, o, lse, st, flags)
+                       : run_window<64>(sh, q, k, v, o, lse, st, flags);
 }
 
 }  // extern "C"

@@ -150,16 +150,6 @@ HS2_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The bounded wait of tc.cuh with its slow part out of line: twelve warps run
-// five roles' code here, and what they share of the instruction cache counts.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                       unsigned* flags) {
-    return mbar_wait(bar, parity, abort, flags);
-}
-HS2_DEV bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* flags) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, flags);
-}
-HS2_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Barrier of the 128 threads of a softmax group; true if any of them passes true.
 HS2_DEV bool group_any(int group, bool pred) {
     uint32_t r;

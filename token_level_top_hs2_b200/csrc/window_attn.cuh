@@ -3,22 +3,57 @@
 // Query i of a chunk of Lq sits at position t = Lk - Lq + i and sees the keys
 // s <= t with s > t - window or s < n_sink:
 //   o = sum_s softmax_s(scale <q, k_s>) v_s,   lse = ln sum_s exp(scale <q, k_s>)
+//
+// The G query heads of a KV head share their keys, so the 128 rows of a
+// tensor-core tile are nt = floor(128 / G) tokens x G heads (row = token * G +
+// head): with 16 heads a tile of 8 tokens and a window of 128 needs 135 keys,
+// where 128 tokens of one head would need 255.  One persistent CTA per SM
+// takes items of two such tiles (2 nt tokens of one KV head), which use the
+// same keys: the sinks, rounded up to 16 rows, then the rows from the first
+// token's window to the last token, in tiles of 64.
+//
+// Both tiles' logits are double-buffered in tensor memory (2 x 2 x 64 columns,
+// beside two accumulators of D), so that QK^T of the tile after next is issued
+// behind PV of this one and a softmax warp finds its next logits there when it
+// is done: the chain softmax -> PV -> QK^T -> softmax of a single buffer is cut.
+//   warp 0      TMA producer: queries (two items), K and V rings
+//   warp 1      MMA issuer (one thread): S_x = Q_x K^T, O_x += P_x V
+//   warp 2      stores finished tiles from shared memory (TMA)
+//   warps 4-7   softmax of tile 0, thread = row = TMEM lane
+//   warps 8-11  softmax of tile 1
+// P (bf16, as V is) overwrites its logits; the running maximum is raised only
+// when a tile exceeds it by 2^8, so the accumulator is rarely rescaled.
 #pragma once
 
-#include "common.cuh"
+#include "tc.cuh"
 
 namespace hs2 {
 namespace win {
 
+using namespace hs2::tc;
+
+constexpr int BM = 128;           // rows of a tile
+constexpr int BN = 64;            // keys of a tile
+constexpr int kThreads = 384;
+constexpr float kRaiseLog2 = 8.f;
+
+struct Shape {
+    int B, Lq, Lk, Hq, Hkv, G, nt, window, n_sink, blocks, items;
+    float scale2;
+};
+
 // One query row and head by one warp, in fp32: the running maximum and sum of
 // the softmax over the visible keys alone, one key at a time, so that nothing
-// a masked row holds (NaN or infinities of a padded batch) is ever read.
-// Lane i owns the D/32 dims from i * D/32.
+// a masked row holds is ever read.  Rows whose tensor-core result is not
+// finite come here: 0 * NaN is NaN there, so that a masked key row of NaN or
+// infinities (the padding of a padded batch) spoils the rows that share its
+// tile.  Lane i owns the D/32 dims from i * D/32.
 template <int D>
-HS2_DEV void attend_row(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-                        const __nv_bfloat16* __restrict__ v, int64_t ld, int t, int window,
-                        int n_sink, float scale2, __nv_bfloat16* __restrict__ o,
-                        float* __restrict__ lse) {
+static __device__ __noinline__ void attend_row(const __nv_bfloat16* __restrict__ q,
+                                        const __nv_bfloat16* __restrict__ k,
+                                        const __nv_bfloat16* __restrict__ v, int64_t ld, int t,
+                                        int window, int n_sink, float scale2,
+                                        __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
     constexpr int E = D / 32;
     const int lane = lane_id();
     float qf[E], acc[E], m = -INFINITY, l = 0.f;
@@ -51,19 +86,448 @@ HS2_DEV void attend_row(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16
     if (lse && lane == 0) *lse = (m + log2f(l)) * kLn2;
 }
 
-// grid: a warp per (sequence, query, head)
+// The keys of an item as a list of entries: [0, pre) are positions 0 .. pre-1
+// (the sinks, rounded up to 16), entry e >= pre is position base + e - pre.
+struct Item {
+    int b, hk, i0, t0;         // sequence, KV head, first query, its position
+    int pre, base, entries, tiles;
+};
+HS2_DEV Item item_of(const Shape& s, int n) {
+    Item it;
+    const int rest = n / s.blocks;
+    it.i0 = (n - rest * s.blocks) * 2 * s.nt;
+    it.b = rest / s.Hkv;
+    it.hk = rest - it.b * s.Hkv;
+    it.t0 = s.Lk - s.Lq + it.i0;
+    const int last = min(s.Lk - 1, it.t0 + 2 * s.nt - 1);
+    const int w0 = max(0, it.t0 - s.window + 1);
+    // sinks that reach into the window's rows, or nearly: one run of rows
+    const bool joined = s.n_sink > w0 - 16;
+    it.base = joined && s.n_sink > 0 ? 0 : w0;
+    it.pre = joined || s.n_sink == 0 ? 0 : (s.n_sink + 15) & ~15;
+    it.entries = it.pre + last + 1 - it.base;
+    it.tiles = (it.entries + BN - 1) / BN;
+    return it;
+}
+// rows of tile j that are loaded: a multiple of 16
+HS2_DEV int rows_of(const Item& it, int j) { return min(BN, (it.entries - j * BN + 15) & ~15); }
+
+// A walk over a CTA's tiles, item by item.
+struct Walk {
+    Item it;
+    int n, j, count;  // item, tile in it, items before it
+    HS2_DEV void start(const Shape& s, int first) {
+        n = first;
+        j = count = 0;
+        if (n < s.items) it = item_of(s, n);
+    }
+    HS2_DEV bool done(const Shape& s) const { return n >= s.items; }
+    HS2_DEV void next(const Shape& s, int step) {
+        if (++j < it.tiles) return;
+        j = 0;
+        count++;
+        n += step;
+        if (n < s.items) it = item_of(s, n);
+    }
+};
+
 template <int D>
-__global__ void __launch_bounds__(128)
-window_rows_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-                   const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ o,
-                   float* __restrict__ lse, int B, int Lq, int Lk, int Hq, int Hkv, int window,
-                   int n_sink, float scale2) {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)B * Lq * Hq) return;
-    const int h = (int)(row % Hq), i = (int)(row / Hq % Lq), b = (int)(row / Hq / Lq);
-    const size_t kv = ((size_t)b * Lk * Hkv + h / (Hq / Hkv)) * D;
-    attend_row<D>(q + row * D, k + kv, v + kv, (int64_t)Hkv * D, Lk - Lq + i, window, n_sink, scale2,
-                  o + row * D, lse ? lse + row : nullptr);
+struct Cfg {
+    static constexpr int DB = D / 64;                // 64-column blocks
+    static constexpr int QT = BM * D * 2;            // one tile's queries
+    static constexpr int KT = BN * D * 2;            // a K or V tile
+    static constexpr int NS = D == 128 ? 3 : 6;      // ring depth
+    static constexpr int OFF_K = 4 * QT;             // (two items of two tiles before it)
+    static constexpr int OFF_V = OFF_K + NS * KT;
+    static constexpr int SMEM = OFF_V + NS * KT + 1024;
+    static constexpr uint32_t COL_O = 256;           // S: [tile][buffer] of 64 columns
+};
+
+struct Bars {
+    uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
+    // [tile][tile number or item number & 1]: a softmax warp can be one ahead of
+    // the thread that waits for it, so each barrier is used every other time
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], staged[2][2];
+    uint64_t stored[2], drain;
+    uint32_t tmem;
+    int abort_;
+};
+
+struct Maps {
+    CUtensorMap q, o;              // [B, L, Hq, D]: 64 columns x G heads x nt tokens
+    CUtensorMap k64, k16, v64, v16;  // [B, Lk, Hkv, D]: 64 columns x 64 or 16 positions
+};
+
+// The low n bits (n <= 0: none, n >= 64: all).
+HS2_DEV uint64_t low_bits(int n) {
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __restrict__ q,
+                   const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse, const Shape sh,
+                   unsigned* __restrict__ flags) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ Bars bars;
+    const int warp = threadIdx.x >> 5, lane = lane_id(), step = gridDim.x;
+    volatile int* abort_ = &bars.abort_;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NS; i++) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 1);
+            for (int j = 0; j < 2; j++) {
+                mbar_init(&bars.s_full[i][j], 1);
+                mbar_init(&bars.p_full[i][j], 4);
+                mbar_init(&bars.pv_done[i][j], 1);
+                mbar_init(&bars.staged[i][j], 4);
+            }
+            mbar_init(&bars.stored[i], 1);
+        }
+        mbar_init(&bars.drain, 1);
+        bars.abort_ = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k64);
+        tma_prefetch_map(&maps.v64);
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = bars.tmem;
+    Walk w;
+    w.start(sh, blockIdx.x);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------------- producer
+            // Queries of the next item go out ahead of this item's last tile.
+            int st = 0, armed = 0, q_armed = 0;
+            uint32_t phase = 1;  // of the empty barriers: the first round passes
+            bool ok = true;
+            auto load_q = [&](const Item& it, int count) {
+                const int set = count & 1;
+                ok = wait(&bars.q_empty[set], ((count >> 1) & 1) ^ 1, abort_, flags);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&bars.q_full[set], 2 * C::DB * 128 * sh.G * sh.nt);
+                for (int x = 0; x < 2; x++)
+                    for (int db = 0; db < C::DB; db++)
+                        tma_load_4d(smem + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
+                                    it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
+                q_armed++;
+            };
+            // rows of a tile: whole, or 16 at a time
+            auto load_rows = [&](uint8_t* dst, const CUtensorMap* m64, const CUtensorMap* m16, int rows,
+                                 uint64_t* bar) {
+                const int e0 = w.j * BN;
+                if (rows == BN && e0 >= w.it.pre) {
+                    for (int db = 0; db < C::DB; db++)
+                        tma_load_4d(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
+                                    w.it.base + e0 - w.it.pre, w.it.b, bar);
+                } else {
+                    for (int r = 0; r < rows; r += 16) {
+                        const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
+                        for (int db = 0; db < C::DB; db++)
+                            tma_load_4d(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
+                                        w.it.b, bar);
+                    }
+                }
+            };
+            if (!w.done(sh)) load_q(w.it, 0);
+            while (ok && !w.done(sh)) {
+                const int rows = rows_of(w.it, w.j);
+                if (!wait(&bars.k_empty[st], phase, abort_, flags)) break;
+                mbar_arrive_expect_tx(&bars.k_full[st], rows * D * 2);
+                load_rows(smem + C::OFF_K + st * C::KT, &maps.k64, &maps.k16, rows, &bars.k_full[st]);
+                if (!wait(&bars.v_empty[st], phase, abort_, flags)) {
+                    volatile int no_abort = 0;
+                    mbar_wait(&bars.k_full[st], phase ^ 1, &no_abort, flags);
+                    break;
+                }
+                mbar_arrive_expect_tx(&bars.v_full[st], rows * D * 2);
+                load_rows(smem + C::OFF_V + st * C::KT, &maps.v64, &maps.v16, rows, &bars.v_full[st]);
+                armed++;
+                if (++st == C::NS) st = 0, phase ^= 1;
+                if (w.j == w.it.tiles - 1 && w.n + step < sh.items)
+                    load_q(item_of(sh, w.n + step), w.count + 1);
+                w.next(sh, step);
+            }
+            if (*abort_) {  // let the copies in flight land before the CTA leaves
+                volatile int no_abort = 0;
+                for (int i = max(0, q_armed - 2); i < q_armed; i++)
+                    mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
+                for (int i = max(0, armed - C::NS); i < armed; i++) {
+                    mbar_wait(&bars.k_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
+                    mbar_wait(&bars.v_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            const uint64_t q0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t k0 = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+            const uint64_t v0 = sdesc_sw128(smem_u32(smem + C::OFF_V), BN * 128, 1024);
+            constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
+            Walk a = w;                      // the tile whose logits are next; w: whose output is
+            int ca = 0, cw = 0, ka = 0, vw = 0;  // their numbers and ring stages
+            uint32_t k_phase = 0, v_phase = 0;
+            auto qk = [&](int x) {
+                if (x == 0) {
+                    if (a.j == 0 &&
+                        !wait(&bars.q_full[a.count & 1], (a.count >> 1) & 1, abort_, flags))
+                        return false;
+                    if (!wait(&bars.k_full[ka], k_phase, abort_, flags)) return false;
+                    fence_after_sync();
+                }
+                const uint32_t id = idesc_bf16_f32(BM, 0, false, false) |
+                                    ((uint32_t)(rows_of(a.it, a.j) >> 3) << 17);
+                const uint64_t dq = q0 + (((2 * (a.count & 1) + x) * C::QT) >> 4);
+                const uint64_t dk = k0 + ((ka * C::KT) >> 4);
+                const uint32_t d = tmem + x * 128 + (ca & 1) * 64;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++)
+                    mma_ss(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
+                           dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
+                mma_commit(&bars.s_full[x][ca & 1]);
+                if (x == 1) {
+                    mma_commit(&bars.k_empty[ka]);
+                    if (++ka == C::NS) ka = 0, k_phase ^= 1;
+                    ca++;
+                    a.next(sh, step);
+                }
+                return true;
+            };
+            auto pv = [&](int x) {
+                if (x == 0 && !wait(&bars.v_full[vw], v_phase, abort_, flags)) return false;
+                if (!wait(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags)) return false;
+                fence_after_sync();
+                const uint64_t dv = v0 + ((vw * C::KT) >> 4);
+                const uint32_t p = tmem + x * 128 + (cw & 1) * 64, d = tmem + C::COL_O + x * D;
+                const int n = rows_of(w.it, w.j) >> 4;
+                for (int ks = 0; ks < n; ks++)
+                    mma_ts(d, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, (w.j > 0 || ks > 0) ? 1u : 0u);
+                mma_commit(&bars.pv_done[x][cw & 1]);
+                if (x == 1) {
+                    mma_commit(&bars.v_empty[vw]);
+                    if (++vw == C::NS) vw = 0, v_phase ^= 1;
+                    cw++;
+                    w.next(sh, step);
+                }
+                return true;
+            };
+            bool ok = true;
+            for (int i = 0; ok && i < 2 && !a.done(sh); i++) ok = qk(0) && qk(1);
+            while (ok && !w.done(sh)) {
+                const bool more = !a.done(sh);
+                // queries two items on wait for this item's outputs to leave their place
+                if (more && a.count - w.count >= 2)
+                    ok = pv(0) && pv(1) && qk(0) && qk(1);
+                else
+                    ok = pv(0) && (!more || qk(0)) && pv(1) && (!more || qk(1));
+            }
+            // every MMA issued must finish before TMEM is released
+            mma_commit(&bars.drain);
+            volatile int no_abort = 0;
+            mbar_wait(&bars.drain, 0, &no_abort, flags);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            // ------------------------------------------------- the stores
+            for (bool ok = true; ok && !w.done(sh); w.count++, w.n += step) {
+                w.it = item_of(sh, w.n);
+                for (int x = 0; ok && x < 2; x++) {
+                    ok = wait(&bars.staged[x][w.count & 1], (w.count >> 1) & 1, abort_, flags);
+                    const int i = w.it.i0 + x * sh.nt;
+                    if (ok && i < sh.Lq)
+                        for (int db = 0; db < C::DB; db++)
+                            tma_store_4d(&maps.o, smem + (2 * (w.count & 1) + x) * C::QT + db * (BM * 128),
+                                         64 * db, w.it.hk * sh.G, i, w.it.b);
+                    bulk_commit();
+                }
+                bulk_wait_read();
+                mbar_arrive(&bars.q_empty[w.count & 1]);
+                bulk_wait();
+                mbar_arrive(&bars.stored[0]);
+                mbar_arrive(&bars.stored[1]);
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------ softmax
+        const int x = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t o_col = lanes + C::COL_O + x * D;
+        const int tok = row / sh.G, head = row - tok * sh.G;
+        bool ok = true;
+        int c = 0;
+        while (ok && !w.done(sh)) {
+            const Item it = w.it;
+            const int i = it.i0 + x * sh.nt + tok, t = it.t0 + x * sh.nt + tok;
+            const bool real = tok < sh.nt && i < sh.Lq;
+            // the row's keys as entries: [0, e_sink) and [e_lo, e_hi)
+            const int e_sink = min(sh.n_sink, t + 1);
+            const int e_lo = it.pre + max(t - sh.window + 1, 0) - it.base;
+            const int e_hi = it.pre + t + 1 - it.base;
+            // entries that every row of the tile sees: past the last row's window
+            // start (or all before it sinks), up to the first row
+            const int t_min = it.t0 + x * sh.nt;
+            const int all_lo = it.pre + max(t_min + sh.nt - sh.window, 0) - it.base;
+            const int all_hi = it.pre + t_min + 1 - it.base;
+            float m = -1e30f, l = 0.f;
+            for (int j = 0; j < it.tiles; j++, c++) {
+                const int e0 = j * BN;
+                const uint32_t s_col = lanes + x * 128 + (c & 1) * 64;
+                ok = __all_sync(~0u, wait(&bars.s_full[x][c & 1], (c >> 1) & 1, abort_, flags));
+                if (!ok) break;
+                fence_after_sync();
+                float s[BN];
+                {
+                    uint32_t r[32];
+                    tmem_ld32(s_col, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 32; u++) s[u] = __uint_as_float(r[u]);
+                    tmem_ld32(s_col + 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 32; u++) s[32 + u] = __uint_as_float(r[u]);
+                }
+                if (!(e0 >= all_lo && e0 + BN <= all_hi)) {
+                    const uint64_t see = low_bits(e_sink - e0) | (low_bits(e_hi - e0) & ~low_bits(e_lo - e0));
+                    const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
+#pragma unroll
+                    for (int u = 0; u < 32; u++) {
+                        s[u] = see0 >> u & 1 ? s[u] : -INFINITY;
+                        s[32 + u] = see1 >> u & 1 ? s[32 + u] : -INFINITY;
+                    }
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int u = 4; u < BN; u += 8)
+#pragma unroll
+                    for (int z = 0; z < 4; z++)
+                        mx[z] = u + 4 + z < BN ? fmax3(mx[z], s[u + z], s[u + 4 + z])
+                                               : fmaxf(mx[z], s[u + z]);
+                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sh.scale2;
+                const bool raise = top > m + kRaiseLog2;
+                if (__any_sync(~0u, raise)) {
+                    const float mn = raise ? top : m;
+                    const float alpha = ex2(m - mn);
+                    m = mn;
+                    l *= alpha;
+                    if (j > 0) {
+                        // O holds the sum up to tile j - 1: once that is there, rescale it
+                        ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
+                                                       abort_, flags));
+                        if (!ok) break;
+                        fence_after_sync();
+#pragma unroll 1
+                        for (int u = 0; u < D; u += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(o_col + u, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int z = 0; z < 16; z++)
+                                r[z] = __float_as_uint(__uint_as_float(r[z]) * alpha);
+                            tmem_st16(o_col + u, r);
+                        }
+                    }
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int u = 0; u < 16; u++) {
+                        const float p0 = ex2(fmaf(s[h * 32 + 2 * u], sh.scale2, -m));
+                        const float p1 = ex2(fmaf(s[h * 32 + 2 * u + 1], sh.scale2, -m));
+                        sum[u & 3] += p0 + p1;
+                        r[u] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(s_col + h * 16, r);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[x][c & 1]);
+            }
+            if (!ok) break;
+            // ------------------------------------- the tile's result
+            ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
+                                                       abort_, flags));
+            if (!ok) break;
+            fence_after_sync();
+            const float inv = 1.f / l;
+            float zero = l * 0.f;  // NaN once anything is not finite
+            // over the tile's queries, which nothing reads any more
+            uint8_t* dst = smem + (2 * (w.count & 1) + x) * C::QT + row * 128;
+#pragma unroll 1
+            for (int u = 0; u < D; u += 32) {
+                uint32_t r[32];
+                tmem_ld32(o_col + u, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int z = 0; z < 32; z += 8) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const float a = __uint_as_float(r[z + 2 * y]) * inv;
+                        const float b = __uint_as_float(r[z + 2 * y + 1]) * inv;
+                        zero = fmaf(a, 0.f, fmaf(b, 0.f, zero));
+                        p[y] = pack_bf16(a, b);
+                    }
+                    *reinterpret_cast<uint4*>(dst + (u >> 6) * (BM * 128) +
+                                              ((((u + z) >> 3) & 7) ^ (row & 7)) * 16) =
+                        make_uint4(p[0], p[1], p[2], p[3]);
+                }
+            }
+            const size_t at = ((size_t)it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head;
+            if (lse && real) lse[at] = (m + __log2f(l)) * kLn2;
+            fence_before_sync();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.staged[x][w.count & 1]);
+            unsigned spoilt = __ballot_sync(~0u, real && !(zero == 0.f));
+            if (spoilt) {
+                ok = __all_sync(~0u, wait(&bars.stored[x], w.count & 1, abort_, flags));
+                if (!ok) break;
+                const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
+                for (; spoilt; spoilt &= spoilt - 1) {
+                    const int src = __ffs(spoilt) - 1;
+                    const size_t a = __shfl_sync(~0u, at, src);
+                    attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
+                                  __shfl_sync(~0u, t, src), sh.window, sh.n_sink, sh.scale2, o + a * D,
+                                  lse ? lse + a : nullptr);
+                }
+            }
+            w.j = it.tiles - 1;
+            w.next(sh, step);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 }  // namespace win
