@@ -17,7 +17,7 @@
 // behind PV of this one and a softmax warp finds its next logits there when it
 // is done: the chain softmax -> PV -> QK^T -> softmax of a single buffer is cut.
 //   warp 0      TMA producer: queries (two items), K and V rings
-//   warp 1      MMA issuer (one thread): S_x = Q_x K^T, O_x += P_x V
+//   warps 1, 3  MMA issuers of tiles 0 and 1: S_x = Q_x K^T, O_x += P_x V
 //   warp 2      stores finished tiles from shared memory (TMA)
 //   warps 4-7   softmax of tile 0, thread = row = TMEM lane
 //   warps 8-11  softmax of tile 1
@@ -148,7 +148,7 @@ struct Bars {
     // [tile][tile number or item number & 1]: a softmax warp can be one ahead of
     // the thread that waits for it, so each barrier is used every other time
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], staged[2][2];
-    uint64_t stored[2], drain;
+    uint64_t stored[2], drain[2];
     uint32_t tmem;
     int abort_;
 };
@@ -174,15 +174,15 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Bars bars;
-    const int warp = threadIdx.x >> 5, lane = lane_id(), step = gridDim.x;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = lane_id(), step = gridDim.x;
     volatile int* abort_ = &bars.abort_;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; i++) {
             mbar_init(&bars.k_full[i], 1);
-            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.k_empty[i], 2);  // both tiles' MMAs
             mbar_init(&bars.v_full[i], 1);
-            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.v_empty[i], 2);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&bars.q_full[i], 1);
@@ -194,8 +194,8 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 mbar_init(&bars.staged[i][j], 4);
             }
             mbar_init(&bars.stored[i], 1);
+            mbar_init(&bars.drain[i], 1);
         }
-        mbar_init(&bars.drain, 1);
         bars.abort_ = 0;
         fence_mbar_init();
     }
@@ -211,143 +211,130 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = __shfl_sync(~0u, bars.tmem, 0);
+    const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
     Walk w;
     w.start(sh, blockIdx.x);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // -------------------------------------------------- producer
-            // Queries of the next item go out ahead of this item's last tile.
-            int st = 0, armed = 0, q_armed = 0;
-            uint32_t phase = 1;  // of the empty barriers: the first round passes
-            bool ok = true;
-            auto load_q = [&](const Item& it, int count) {
-                const int set = count & 1;
-                ok = wait(&bars.q_empty[set], ((count >> 1) & 1) ^ 1, abort_, flags);
-                if (!ok) return;
-                mbar_arrive_expect_tx(&bars.q_full[set], 2 * C::DB * 128 * sh.G * sh.nt);
-                for (int x = 0; x < 2; x++)
+        // -------------------------------------------------- producer
+        // Queries of the next item go out ahead of this item's last tile.
+        int st = 0, armed = 0, q_armed = 0;
+        uint32_t phase = 1;  // of the empty barriers: the first round passes
+        bool ok = true;
+        auto load_q = [&](const Item& it, int count) {
+            const int set = count & 1;
+            ok = wait_warp(&bars.q_empty[set], ((count >> 1) & 1) ^ 1, abort_, flags);
+            if (!ok) return;
+            mbar_arrive_expect_tx_w(&bars.q_full[set], 2 * C::DB * 128 * sh.G * sh.nt);
+            for (int x = 0; x < 2; x++)
+                for (int db = 0; db < C::DB; db++)
+                    tma_load_4d_w(base + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
+                                it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
+            q_armed++;
+        };
+        // rows of a tile: whole, or 16 at a time
+        auto load_rows = [&](uint32_t dst, const CUtensorMap* m64, const CUtensorMap* m16, int rows,
+                             uint64_t* bar) {
+            const int e0 = w.j * BN;
+            if (rows == BN && e0 >= w.it.pre) {
+                for (int db = 0; db < C::DB; db++)
+                    tma_load_4d_w(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
+                                w.it.base + e0 - w.it.pre, w.it.b, bar);
+            } else {
+                for (int r = 0; r < rows; r += 16) {
+                    const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
                     for (int db = 0; db < C::DB; db++)
-                        tma_load_4d(smem + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
-                                    it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
-                q_armed++;
-            };
-            // rows of a tile: whole, or 16 at a time
-            auto load_rows = [&](uint8_t* dst, const CUtensorMap* m64, const CUtensorMap* m16, int rows,
-                                 uint64_t* bar) {
-                const int e0 = w.j * BN;
-                if (rows == BN && e0 >= w.it.pre) {
-                    for (int db = 0; db < C::DB; db++)
-                        tma_load_4d(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
-                                    w.it.base + e0 - w.it.pre, w.it.b, bar);
-                } else {
-                    for (int r = 0; r < rows; r += 16) {
-                        const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
-                        for (int db = 0; db < C::DB; db++)
-                            tma_load_4d(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
-                                        w.it.b, bar);
-                    }
+                        tma_load_4d_w(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
+                                    w.it.b, bar);
                 }
-            };
-            if (!w.done(sh)) load_q(w.it, 0);
-            while (ok && !w.done(sh)) {
-                const int rows = rows_of(w.it, w.j);
-                if (!wait(&bars.k_empty[st], phase, abort_, flags)) break;
-                mbar_arrive_expect_tx(&bars.k_full[st], rows * D * 2);
-                load_rows(smem + C::OFF_K + st * C::KT, &maps.k64, &maps.k16, rows, &bars.k_full[st]);
-                if (!wait(&bars.v_empty[st], phase, abort_, flags)) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&bars.k_full[st], phase ^ 1, &no_abort, flags);
-                    break;
-                }
-                mbar_arrive_expect_tx(&bars.v_full[st], rows * D * 2);
-                load_rows(smem + C::OFF_V + st * C::KT, &maps.v64, &maps.v16, rows, &bars.v_full[st]);
-                armed++;
-                if (++st == C::NS) st = 0, phase ^= 1;
-                if (w.j == w.it.tiles - 1 && w.n + step < sh.items)
-                    load_q(item_of(sh, w.n + step), w.count + 1);
-                w.next(sh, step);
             }
-            if (*abort_) {  // let the copies in flight land before the CTA leaves
+        };
+        if (!w.done(sh)) load_q(w.it, 0);
+        while (ok && !w.done(sh)) {
+            const int rows = rows_of(w.it, w.j);
+            if (!wait_warp(&bars.k_empty[st], phase, abort_, flags)) break;
+            mbar_arrive_expect_tx_w(&bars.k_full[st], rows * D * 2);
+            load_rows(base + C::OFF_K + st * C::KT, &maps.k64, &maps.k16, rows, &bars.k_full[st]);
+            if (!wait_warp(&bars.v_empty[st], phase, abort_, flags)) {
                 volatile int no_abort = 0;
-                for (int i = max(0, q_armed - 2); i < q_armed; i++)
-                    mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
-                for (int i = max(0, armed - C::NS); i < armed; i++) {
-                    mbar_wait(&bars.k_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
-                    mbar_wait(&bars.v_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
-                }
+                mbar_wait(&bars.k_full[st], phase ^ 1, &no_abort, flags);
+                break;
             }
+            mbar_arrive_expect_tx_w(&bars.v_full[st], rows * D * 2);
+            load_rows(base + C::OFF_V + st * C::KT, &maps.v64, &maps.v16, rows, &bars.v_full[st]);
+            armed++;
+            if (++st == C::NS) st = 0, phase ^= 1;
+            if (w.j == w.it.tiles - 1 && w.n + step < sh.items)
+                load_q(item_of(sh, w.n + step), w.count + 1);
+            w.next(sh, step);
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------ MMA issuer
-            const uint64_t q0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-            const uint64_t k0 = sdesc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-            const uint64_t v0 = sdesc_sw128(smem_u32(smem + C::OFF_V), BN * 128, 1024);
-            constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
-            Walk a = w;                      // the tile whose logits are next; w: whose output is
-            int ca = 0, cw = 0, ka = 0, vw = 0;  // their numbers and ring stages
-            uint32_t k_phase = 0, v_phase = 0;
-            auto qk = [&](int x) {
-                if (x == 0) {
-                    if (a.j == 0 &&
-                        !wait(&bars.q_full[a.count & 1], (a.count >> 1) & 1, abort_, flags))
-                        return false;
-                    if (!wait(&bars.k_full[ka], k_phase, abort_, flags)) return false;
-                    fence_after_sync();
-                }
-                const uint32_t id = idesc_bf16_f32(BM, 0, false, false) |
-                                    ((uint32_t)(rows_of(a.it, a.j) >> 3) << 17);
-                const uint64_t dq = q0 + (((2 * (a.count & 1) + x) * C::QT) >> 4);
-                const uint64_t dk = k0 + ((ka * C::KT) >> 4);
-                const uint32_t d = tmem + x * 128 + (ca & 1) * 64;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ks++)
-                    mma_ss(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
-                           dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
-                mma_commit(&bars.s_full[x][ca & 1]);
-                if (x == 1) {
-                    mma_commit(&bars.k_empty[ka]);
-                    if (++ka == C::NS) ka = 0, k_phase ^= 1;
-                    ca++;
-                    a.next(sh, step);
-                }
-                return true;
-            };
-            auto pv = [&](int x) {
-                if (x == 0 && !wait(&bars.v_full[vw], v_phase, abort_, flags)) return false;
-                if (!wait(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags)) return false;
-                fence_after_sync();
-                const uint64_t dv = v0 + ((vw * C::KT) >> 4);
-                const uint32_t p = tmem + x * 128 + (cw & 1) * 64, d = tmem + C::COL_O + x * D;
-                const int n = rows_of(w.it, w.j) >> 4;
-                for (int ks = 0; ks < n; ks++)
-                    mma_ts(d, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, (w.j > 0 || ks > 0) ? 1u : 0u);
-                mma_commit(&bars.pv_done[x][cw & 1]);
-                if (x == 1) {
-                    mma_commit(&bars.v_empty[vw]);
-                    if (++vw == C::NS) vw = 0, v_phase ^= 1;
-                    cw++;
-                    w.next(sh, step);
-                }
-                return true;
-            };
-            bool ok = true;
-            for (int i = 0; ok && i < 2 && !a.done(sh); i++) ok = qk(0) && qk(1);
-            while (ok && !w.done(sh)) {
-                const bool more = !a.done(sh);
-                // queries two items on wait for this item's outputs to leave their place
-                if (more && a.count - w.count >= 2)
-                    ok = pv(0) && pv(1) && qk(0) && qk(1);
-                else
-                    ok = pv(0) && (!more || qk(0)) && pv(1) && (!more || qk(1));
-            }
-            // every MMA issued must finish before TMEM is released
-            mma_commit(&bars.drain);
+        if (*abort_) {  // let the copies in flight land before the CTA leaves
             volatile int no_abort = 0;
-            mbar_wait(&bars.drain, 0, &no_abort, flags);
+            for (int i = max(0, q_armed - 2); i < q_armed; i++)
+                mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
+            for (int i = max(0, armed - C::NS); i < armed; i++) {
+                mbar_wait(&bars.k_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
+                mbar_wait(&bars.v_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
+            }
         }
+    } else if (warp == 1 || warp == 3) {
+        // ----------------------------------------------- MMA issuers
+        const int x = warp >> 1;
+        const uint64_t q0 = sdesc_sw128(base + x * C::QT, 16, 1024);
+        const uint64_t k0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
+        const uint64_t v0 = sdesc_sw128(base + C::OFF_V, BN * 128, 1024);
+        constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
+        const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
+        Walk a = w;                      // the tile whose logits are next; w: whose output is
+        int ca = 0, cw = 0, ka = 0, vw = 0;  // their numbers and ring stages
+        uint32_t k_phase = 0, v_phase = 0;
+        auto qk = [&]() {
+            if (a.j == 0 && !wait_warp(&bars.q_full[a.count & 1], (a.count >> 1) & 1, abort_, flags))
+                return false;
+            if (!wait_warp(&bars.k_full[ka], k_phase, abort_, flags)) return false;
+            fence_after_sync();
+            const uint32_t id = idesc_bf16_f32(BM, 0, false, false) |
+                                ((uint32_t)(rows_of(a.it, a.j) >> 3) << 17);
+            const uint64_t dq = q0 + ((2 * (a.count & 1) * C::QT) >> 4);
+            const uint64_t dk = k0 + ((ka * C::KT) >> 4);
+            const uint32_t d = s_col + (ca & 1) * 64;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks++)
+                mma_ss_w(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
+                         dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
+            mma_commit_w(&bars.s_full[x][ca & 1]);
+            mma_commit_w(&bars.k_empty[ka]);
+            if (++ka == C::NS) ka = 0, k_phase ^= 1;
+            ca++;
+            a.next(sh, step);
+            return true;
+        };
+        auto pv = [&]() {
+            if (!wait_warp(&bars.v_full[vw], v_phase, abort_, flags)) return false;
+            if (!wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags)) return false;
+            fence_after_sync();
+            const uint64_t dv = v0 + ((vw * C::KT) >> 4);
+            const uint32_t p = s_col + (cw & 1) * 64;
+            const int n = rows_of(w.it, w.j) >> 4;
+            mma_ts_w(o_col, p, dv, id_pv, w.j > 0);
+#pragma unroll
+            for (int ks = 1; ks < BN / 16; ks++)
+                if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
+            mma_commit_w(&bars.pv_done[x][cw & 1]);
+            mma_commit_w(&bars.v_empty[vw]);
+            if (++vw == C::NS) vw = 0, v_phase ^= 1;
+            cw++;
+            w.next(sh, step);
+            return true;
+        };
+        bool ok = true;
+        for (int i = 0; ok && i < 2 && !a.done(sh); i++) ok = qk();
+        while (ok && !w.done(sh)) ok = pv() && (a.done(sh) || qk());
+        // every MMA issued must finish before TMEM is released
+        mma_commit_w(&bars.drain[x]);
+        volatile int no_abort = 0;
+        mbar_wait(&bars.drain[x], 0, &no_abort, flags);
     } else if (warp == 2) {
         if (lane == 0) {
             // ------------------------------------------------- the stores
