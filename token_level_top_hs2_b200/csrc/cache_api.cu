@@ -163,7 +163,6 @@ hs2_status run_window(const win::Shape& s, const void* q, const void* k, const v
                       float* lse, cudaStream_t st, unsigned* flags) {
     win::Maps m;
     if (!map_rows(&m.q, q, s.B, s.Lq, s.Hq, D, s.G, s.nt) ||
-        !map_rows(&m.o, o, s.B, s.Lq, s.Hq, D, s.G, s.nt) ||
         !map_rows(&m.k64, k, s.B, s.Lk, s.Hkv, D, 1, win::BN) ||
         !map_rows(&m.k16, k, s.B, s.Lk, s.Hkv, D, 1, 16) ||
         !map_rows(&m.v64, v, s.B, s.Lk, s.Hkv, D, 1, win::BN) ||
@@ -321,7 +320,9 @@ hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const v
     if (!flags) return HS2_ERR_CUDA;
     const int G = s->Hq / s->Hkv, nt = win::BM / G;
     const int64_t blocks = ((int64_t)s->Lq + 2 * nt - 1) / (2 * nt);
-    if (blocks * s->B * s->Hkv > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    // items and rows are counted in 32 bits
+    if (blocks * s->B * s->Hkv > INT_MAX || (int64_t)s->B * s->Lq * s->Hq > INT_MAX)
+        return HS2_ERR_UNSUPPORTED;
     const win::Shape sh = {s->B, s->Lq, s->Lk, s->Hq, s->Hkv, G, nt, s->window, s->n_sink, (int)blocks,
                            (int)(blocks * s->B * s->Hkv), s->scale * kLog2e};
     return s->d == 128 ? run_window<128>(sh, q, k, v, o, lse, st, flags)

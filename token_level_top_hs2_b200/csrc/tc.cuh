@@ -125,19 +125,6 @@ HS2_DEV void tma_load_3d_hint(void* dst, const CUtensorMap* map, int x, int y, i
         "l"(policy)
         : "memory");
 }
-// Tiled tensor store from this CTA's shared memory, in the thread's current
-// bulk group; rows past the tensor's end are left out.
-HS2_DEV void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-            reinterpret_cast<uint64_t>(map)),
-        "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(src))
-        : "memory");
-}
-HS2_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// The thread's bulk stores have read their shared memory / are complete.
-HS2_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-HS2_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 HS2_DEV void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

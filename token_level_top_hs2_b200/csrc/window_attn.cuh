@@ -16,9 +16,8 @@
 // beside two accumulators of D), so that QK^T of the tile after next is issued
 // behind PV of this one and a softmax warp finds its next logits there when it
 // is done: the chain softmax -> PV -> QK^T -> softmax of a single buffer is cut.
-//   warp 0      TMA producer: queries (two items), K and V rings
+//   warps 0, 2  TMA producers: queries (two items) and the K ring; the V ring
 //   warps 1, 3  MMA issuers of tiles 0 and 1: S_x = Q_x K^T, O_x += P_x V
-//   warp 2      stores finished tiles from shared memory (TMA)
 //   warps 4-7   softmax of tile 0, thread = row = TMEM lane
 //   warps 8-11  softmax of tile 1
 // P (bf16, as V is) overwrites its logits; the running maximum is raised only
@@ -136,32 +135,31 @@ struct Cfg {
     static constexpr int DB = D / 64;                // 64-column blocks
     static constexpr int QT = BM * D * 2;            // one tile's queries
     static constexpr int KT = BN * D * 2;            // a K or V tile
-    static constexpr int NS = D == 128 ? 3 : 6;      // ring depth
+    static constexpr int NK = D == 128 ? 3 : 6;      // ring depths
+    static constexpr int NV = D == 128 ? 2 : 6;
     static constexpr int OFF_K = 4 * QT;             // (two items of two tiles before it)
-    static constexpr int OFF_V = OFF_K + NS * KT;
-    static constexpr int SMEM = OFF_V + NS * KT + 1024;
+    static constexpr int OFF_V = OFF_K + NK * KT;
+    static constexpr int OFF_O = OFF_V + NV * KT;    // 32 rows x 32 columns per softmax warp
+    static constexpr int SMEM = OFF_O + 8 * 2048 + 1024;
     static constexpr uint32_t COL_O = 256;           // S: [tile][buffer] of 64 columns
 };
 
 struct Bars {
     uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
-    // [tile][tile number or item number & 1]: a softmax warp can be one ahead of
-    // the thread that waits for it, so each barrier is used every other time
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], staged[2][2];
-    uint64_t stored[2], drain[2];
+    // [tile][tile number & 1]: a softmax warp can be one ahead of the thread
+    // that waits for it, so each barrier is used every other time
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
     uint32_t tmem;
     int abort_;
 };
 
 struct Maps {
-    CUtensorMap q, o;              // [B, L, Hq, D]: 64 columns x G heads x nt tokens
+    CUtensorMap q;                   // [B, Lq, Hq, D]: 64 columns x G heads x nt tokens
     CUtensorMap k64, k16, v64, v16;  // [B, Lk, Hkv, D]: 64 columns x 64 or 16 positions
 };
 
-// The low n bits (n <= 0: none, n >= 64: all).
-HS2_DEV uint64_t low_bits(int n) {
-    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
-}
+// The low n bits (n <= 0: none, n >= 32: all).
+HS2_DEV uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -178,23 +176,23 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     volatile int* abort_ = &bars.abort_;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NS; i++) {
+        for (int i = 0; i < C::NK; i++) {
             mbar_init(&bars.k_full[i], 1);
             mbar_init(&bars.k_empty[i], 2);  // both tiles' MMAs
+        }
+        for (int i = 0; i < C::NV; i++) {
             mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.v_empty[i], 2);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.q_empty[i], 2);
+            mbar_init(&bars.drain[i], 1);
             for (int j = 0; j < 2; j++) {
                 mbar_init(&bars.s_full[i][j], 1);
                 mbar_init(&bars.p_full[i][j], 4);
                 mbar_init(&bars.pv_done[i][j], 1);
-                mbar_init(&bars.staged[i][j], 4);
             }
-            mbar_init(&bars.stored[i], 1);
-            mbar_init(&bars.drain[i], 1);
         }
         bars.abort_ = 0;
         fence_mbar_init();
@@ -216,9 +214,17 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     Walk w;
     w.start(sh, blockIdx.x);
 
-    if (warp == 0) {
-        // -------------------------------------------------- producer
-        // Queries of the next item go out ahead of this item's last tile.
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------- producers
+        // Warp 0 loads queries and K, warp 2 V.  The queries of the next item
+        // go out ahead of this item's last tile.
+        const bool is_v = warp == 2;
+        const CUtensorMap* m64 = is_v ? &maps.v64 : &maps.k64;
+        const CUtensorMap* m16 = is_v ? &maps.v16 : &maps.k16;
+        uint64_t* full = is_v ? bars.v_full : bars.k_full;
+        uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+        const uint32_t ring = base + (is_v ? C::OFF_V : C::OFF_K);
+        const int depth = is_v ? C::NV : C::NK;
         int st = 0, armed = 0, q_armed = 0;
         uint32_t phase = 1;  // of the empty barriers: the first round passes
         bool ok = true;
@@ -230,42 +236,30 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             for (int x = 0; x < 2; x++)
                 for (int db = 0; db < C::DB; db++)
                     tma_load_4d_w(base + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
-                                it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
+                                  it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
             q_armed++;
         };
-        // rows of a tile: whole, or 16 at a time
-        auto load_rows = [&](uint32_t dst, const CUtensorMap* m64, const CUtensorMap* m16, int rows,
-                             uint64_t* bar) {
-            const int e0 = w.j * BN;
+        if (!is_v && !w.done(sh)) load_q(w.it, 0);
+        while (ok && !w.done(sh)) {
+            const int rows = rows_of(w.it, w.j), e0 = w.j * BN;
+            if (!wait_warp(&empty[st], phase, abort_, flags)) break;
+            mbar_arrive_expect_tx_w(&full[st], rows * D * 2);
+            const uint32_t dst = ring + st * C::KT;
             if (rows == BN && e0 >= w.it.pre) {
                 for (int db = 0; db < C::DB; db++)
                     tma_load_4d_w(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
-                                w.it.base + e0 - w.it.pre, w.it.b, bar);
+                                  w.it.base + e0 - w.it.pre, w.it.b, &full[st]);
             } else {
                 for (int r = 0; r < rows; r += 16) {
                     const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
                     for (int db = 0; db < C::DB; db++)
                         tma_load_4d_w(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
-                                    w.it.b, bar);
+                                      w.it.b, &full[st]);
                 }
             }
-        };
-        if (!w.done(sh)) load_q(w.it, 0);
-        while (ok && !w.done(sh)) {
-            const int rows = rows_of(w.it, w.j);
-            if (!wait_warp(&bars.k_empty[st], phase, abort_, flags)) break;
-            mbar_arrive_expect_tx_w(&bars.k_full[st], rows * D * 2);
-            load_rows(base + C::OFF_K + st * C::KT, &maps.k64, &maps.k16, rows, &bars.k_full[st]);
-            if (!wait_warp(&bars.v_empty[st], phase, abort_, flags)) {
-                volatile int no_abort = 0;
-                mbar_wait(&bars.k_full[st], phase ^ 1, &no_abort, flags);
-                break;
-            }
-            mbar_arrive_expect_tx_w(&bars.v_full[st], rows * D * 2);
-            load_rows(base + C::OFF_V + st * C::KT, &maps.v64, &maps.v16, rows, &bars.v_full[st]);
             armed++;
-            if (++st == C::NS) st = 0, phase ^= 1;
-            if (w.j == w.it.tiles - 1 && w.n + step < sh.items)
+            if (++st == depth) st = 0, phase ^= 1;
+            if (!is_v && w.j == w.it.tiles - 1 && w.n + step < sh.items)
                 load_q(item_of(sh, w.n + step), w.count + 1);
             w.next(sh, step);
         }
@@ -273,10 +267,8 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             volatile int no_abort = 0;
             for (int i = max(0, q_armed - 2); i < q_armed; i++)
                 mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
-            for (int i = max(0, armed - C::NS); i < armed; i++) {
-                mbar_wait(&bars.k_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
-                mbar_wait(&bars.v_full[i % C::NS], (i / C::NS) & 1, &no_abort, flags);
-            }
+            for (int i = max(0, armed - depth); i < armed; i++)
+                mbar_wait(&full[i % depth], (i / depth) & 1, &no_abort, flags);
         }
     } else if (warp == 1 || warp == 3) {
         // ----------------------------------------------- MMA issuers
@@ -305,7 +297,8 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                          dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
             mma_commit_w(&bars.s_full[x][ca & 1]);
             mma_commit_w(&bars.k_empty[ka]);
-            if (++ka == C::NS) ka = 0, k_phase ^= 1;
+            if (a.j == a.it.tiles - 1) mma_commit_w(&bars.q_empty[a.count & 1]);
+            if (++ka == C::NK) ka = 0, k_phase ^= 1;
             ca++;
             a.next(sh, step);
             return true;
@@ -323,7 +316,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
             mma_commit_w(&bars.pv_done[x][cw & 1]);
             mma_commit_w(&bars.v_empty[vw]);
-            if (++vw == C::NS) vw = 0, v_phase ^= 1;
+            if (++vw == C::NV) vw = 0, v_phase ^= 1;
             cw++;
             w.next(sh, step);
             return true;
@@ -335,28 +328,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         mma_commit_w(&bars.drain[x]);
         volatile int no_abort = 0;
         mbar_wait(&bars.drain[x], 0, &no_abort, flags);
-    } else if (warp == 2) {
-        if (lane == 0) {
-            // ------------------------------------------------- the stores
-            for (bool ok = true; ok && !w.done(sh); w.count++, w.n += step) {
-                w.it = item_of(sh, w.n);
-                for (int x = 0; ok && x < 2; x++) {
-                    ok = wait(&bars.staged[x][w.count & 1], (w.count >> 1) & 1, abort_, flags);
-                    const int i = w.it.i0 + x * sh.nt;
-                    if (ok && i < sh.Lq)
-                        for (int db = 0; db < C::DB; db++)
-                            tma_store_4d(&maps.o, smem + (2 * (w.count & 1) + x) * C::QT + db * (BM * 128),
-                                         64 * db, w.it.hk * sh.G, i, w.it.b);
-                    bulk_commit();
-                }
-                bulk_wait_read();
-                mbar_arrive(&bars.q_empty[w.count & 1]);
-                bulk_wait();
-                mbar_arrive(&bars.stored[0]);
-                mbar_arrive(&bars.stored[1]);
-            }
-        }
-    } else if (warp >= 4) {
+    } else {
         // ------------------------------------------------------ softmax
         const int x = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -364,54 +336,106 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         const int tok = row / sh.G, head = row - tok * sh.G;
         bool ok = true;
         int c = 0;
+        // The result of an item's tile is taken while the next item's first
+        // weights wait to be used: PV of its last tile is done by then.
+        uint4* stage = reinterpret_cast<uint4*>(smem + C::OFF_O + (warp - 4) * 2048);
+        auto finish = [&](const Item& it, float m, float l) {
+            ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1, abort_, flags));
+            if (!ok) return;
+            fence_after_sync();
+            const int i = it.i0 + x * sh.nt + tok;
+            const bool real = tok < sh.nt && i < sh.Lq;
+            const float inv = 1.f / l;
+            // NaN once anything is not finite
+            __nv_bfloat162 zero = __float2bfloat162_rn(l * 0.f);
+            const __nv_bfloat162 nought = __float2bfloat162_rn(0.f);
+            const int at = real ? (it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head : -1;
+            // through the warp's shared memory, 32 columns at a time, so that
+            // each store instruction writes whole 64-byte pieces of eight rows
+#pragma unroll 1
+            for (int u = 0; u < D; u += 32) {
+                uint32_t r[32];
+                tmem_ld32(o_col + u, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int z = 0; z < 4; z++) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const __nv_bfloat162 v =
+                            __floats2bfloat162_rn(__uint_as_float(r[8 * z + 2 * y]) * inv,
+                                                  __uint_as_float(r[8 * z + 2 * y + 1]) * inv);
+                        zero = __hfma2(v, nought, zero);
+                        p[y] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    stage[lane * 4 + ((z + (lane >> 1)) & 3)] = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int z = 0; z < 4; z++) {
+                    const int r8 = z * 8 + (lane >> 2), to = __shfl_sync(~0u, at, r8);
+                    const uint4 v = stage[r8 * 4 + (((lane & 3) + (r8 >> 1)) & 3)];
+                    if (to >= 0) *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 3) * 8) = v;
+                }
+                __syncwarp();
+            }
+            if (lse && real) lse[at] = (m + __log2f(l)) * kLn2;
+            const bool fine = __low2float(zero) + __high2float(zero) == 0.f;
+            unsigned spoilt = __ballot_sync(~0u, real && !fine);
+            const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
+            for (; spoilt; spoilt &= spoilt - 1) {
+                const int src = __ffs(spoilt) - 1;
+                const size_t a = __shfl_sync(~0u, at, src);
+                attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
+                              it.t0 + __shfl_sync(~0u, i, src) - it.i0, sh.window, sh.n_sink, sh.scale2,
+                              o + a * D, lse ? lse + a : nullptr);
+            }
+        };
+        Item was = w.it;
+        float m_was = 0.f, l_was = 1.f;
         while (ok && !w.done(sh)) {
             const Item it = w.it;
-            const int i = it.i0 + x * sh.nt + tok, t = it.t0 + x * sh.nt + tok;
-            const bool real = tok < sh.nt && i < sh.Lq;
+            const int t = it.t0 + x * sh.nt + tok;
             // the row's keys as entries: [0, e_sink) and [e_lo, e_hi)
             const int e_sink = min(sh.n_sink, t + 1);
             const int e_lo = it.pre + max(t - sh.window + 1, 0) - it.base;
             const int e_hi = it.pre + t + 1 - it.base;
-            // entries that every row of the tile sees: past the last row's window
-            // start (or all before it sinks), up to the first row
+            // entries that every row of the tile sees: from the last row's window
+            // start up to the first row
             const int t_min = it.t0 + x * sh.nt;
             const int all_lo = it.pre + max(t_min + sh.nt - sh.window, 0) - it.base;
             const int all_hi = it.pre + t_min + 1 - it.base;
             float m = -1e30f, l = 0.f;
             for (int j = 0; j < it.tiles; j++, c++) {
                 const int e0 = j * BN;
+                const bool second = e0 + 32 < it.entries;  // (else PV reads the first 32 keys at most)
                 const uint32_t s_col = lanes + x * 128 + (c & 1) * 64;
                 ok = __all_sync(~0u, wait(&bars.s_full[x][c & 1], (c >> 1) & 1, abort_, flags));
                 if (!ok) break;
                 fence_after_sync();
-                float s[BN];
-                {
+                float s[BN], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    if (h == 1 && !second) break;
                     uint32_t r[32];
-                    tmem_ld32(s_col, r);
+                    tmem_ld32(s_col + h * 32, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int u = 0; u < 32; u++) s[u] = __uint_as_float(r[u]);
-                    tmem_ld32(s_col + 32, r);
-                    tmem_ld_wait();
+                    for (int u = 0; u < 32; u++) s[h * 32 + u] = __uint_as_float(r[u]);
+                    const int e = e0 + h * 32;
+                    if (!(e >= all_lo && e + 32 <= all_hi)) {
+                        const uint32_t see =
+                            low_bits(e_sink - e) | (low_bits(e_hi - e) & ~low_bits(e_lo - e));
 #pragma unroll
-                    for (int u = 0; u < 32; u++) s[32 + u] = __uint_as_float(r[u]);
-                }
-                if (!(e0 >= all_lo && e0 + BN <= all_hi)) {
-                    const uint64_t see = low_bits(e_sink - e0) | (low_bits(e_hi - e0) & ~low_bits(e_lo - e0));
-                    const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
-#pragma unroll
-                    for (int u = 0; u < 32; u++) {
-                        s[u] = see0 >> u & 1 ? s[u] : -INFINITY;
-                        s[32 + u] = see1 >> u & 1 ? s[32 + u] : -INFINITY;
+                        for (int u = 0; u < 32; u++)
+                            s[h * 32 + u] = see >> u & 1 ? s[h * 32 + u] : -INFINITY;
                     }
+#pragma unroll
+                    for (int u = 0; u < 32; u += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; z++)
+                            mx[z] = fmax3(mx[z], s[h * 32 + u + z], s[h * 32 + u + 4 + z]);
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int u = 4; u < BN; u += 8)
-#pragma unroll
-                    for (int z = 0; z < 4; z++)
-                        mx[z] = u + 4 + z < BN ? fmax3(mx[z], s[u + z], s[u + 4 + z])
-                                               : fmaxf(mx[z], s[u + z]);
                 const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sh.scale2;
                 const bool raise = top > m + kRaiseLog2;
                 if (__any_sync(~0u, raise)) {
@@ -422,7 +446,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                     if (j > 0) {
                         // O holds the sum up to tile j - 1: once that is there, rescale it
                         ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
-                                                       abort_, flags));
+                                                  abort_, flags));
                         if (!ok) break;
                         fence_after_sync();
 #pragma unroll 1
@@ -440,6 +464,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
+                    if (h == 1 && !second) break;
                     uint32_t r[16];
 #pragma unroll
                     for (int u = 0; u < 16; u++) {
@@ -452,62 +477,19 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
+                if (j == 0 && w.count > 0) {
+                    finish(was, m_was, l_was);
+                    if (!ok) break;
+                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[x][c & 1]);
             }
-            if (!ok) break;
-            // ------------------------------------- the tile's result
-            ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
-                                                       abort_, flags));
-            if (!ok) break;
-            fence_after_sync();
-            const float inv = 1.f / l;
-            float zero = l * 0.f;  // NaN once anything is not finite
-            // over the tile's queries, which nothing reads any more
-            uint8_t* dst = smem + (2 * (w.count & 1) + x) * C::QT + row * 128;
-#pragma unroll 1
-            for (int u = 0; u < D; u += 32) {
-                uint32_t r[32];
-                tmem_ld32(o_col + u, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int z = 0; z < 32; z += 8) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const float a = __uint_as_float(r[z + 2 * y]) * inv;
-                        const float b = __uint_as_float(r[z + 2 * y + 1]) * inv;
-                        zero = fmaf(a, 0.f, fmaf(b, 0.f, zero));
-                        p[y] = pack_bf16(a, b);
-                    }
-                    *reinterpret_cast<uint4*>(dst + (u >> 6) * (BM * 128) +
-                                              ((((u + z) >> 3) & 7) ^ (row & 7)) * 16) =
-                        make_uint4(p[0], p[1], p[2], p[3]);
-                }
-            }
-            const size_t at = ((size_t)it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head;
-            if (lse && real) lse[at] = (m + __log2f(l)) * kLn2;
-            fence_before_sync();
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.staged[x][w.count & 1]);
-            unsigned spoilt = __ballot_sync(~0u, real && !(zero == 0.f));
-            if (spoilt) {
-                ok = __all_sync(~0u, wait(&bars.stored[x], w.count & 1, abort_, flags));
-                if (!ok) break;
-                const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
-                for (; spoilt; spoilt &= spoilt - 1) {
-                    const int src = __ffs(spoilt) - 1;
-                    const size_t a = __shfl_sync(~0u, at, src);
-                    attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
-                                  __shfl_sync(~0u, t, src), sh.window, sh.n_sink, sh.scale2, o + a * D,
-                                  lse ? lse + a : nullptr);
-                }
-            }
+            was = it, m_was = m, l_was = l;
             w.j = it.tiles - 1;
             w.next(sh, step);
         }
+        if (ok && w.count > 0) finish(was, m_was, l_was);
     }
     fence_before_sync();
     __syncthreads();
