@@ -135,19 +135,20 @@ struct Cfg {
     static constexpr int DB = D / 64;                // 64-column blocks
     static constexpr int QT = BM * D * 2;            // one tile's queries
     static constexpr int KT = BN * D * 2;            // a K or V tile
-    static constexpr int NK = D == 128 ? 3 : 6;      // ring depths
-    static constexpr int NV = D == 128 ? 2 : 6;
     static constexpr int OFF_K = 4 * QT;             // (two items of two tiles before it)
-    static constexpr int OFF_V = OFF_K + NK * KT;
-    static constexpr int OFF_O = OFF_V + NV * KT;    // 32 rows x 32 columns per softmax warp
+    static constexpr int OFF_V = OFF_K + 2 * KT;
+    static constexpr int OFF_O = OFF_V + 2 * KT;     // 32 rows x 32 columns per softmax warp
     static constexpr int SMEM = OFF_O + 8 * 2048 + 1024;
     static constexpr uint32_t COL_O = 256;           // S: [tile][buffer] of 64 columns
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
-    // [tile][tile number & 1]: a softmax warp can be one ahead of the thread
-    // that waits for it, so each barrier is used every other time
+    uint64_t q_full[2], q_empty[2];  // [item & 1]
+    // [tile & 1]: K and V have two places; that of tile c is free for tile c + 2
+    // once both rows' tiles have taken theirs (s_full, pv_done)
+    uint64_t k_full[2], v_full[2];
+    // [rows' tile][tile & 1]: a softmax warp can be one ahead of the thread that
+    // waits for it, so each barrier is used every other time
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
     uint32_t tmem;
     int abort_;
@@ -176,17 +177,11 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     volatile int* abort_ = &bars.abort_;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NK; i++) {
-            mbar_init(&bars.k_full[i], 1);
-            mbar_init(&bars.k_empty[i], 2);  // both tiles' MMAs
-        }
-        for (int i = 0; i < C::NV; i++) {
-            mbar_init(&bars.v_full[i], 1);
-            mbar_init(&bars.v_empty[i], 2);
-        }
         for (int i = 0; i < 2; i++) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 2);
+            mbar_init(&bars.q_empty[i], 2);  // both tiles' MMAs
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.drain[i], 1);
             for (int j = 0; j < 2; j++) {
                 mbar_init(&bars.s_full[i][j], 1);
@@ -222,11 +217,9 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         const CUtensorMap* m64 = is_v ? &maps.v64 : &maps.k64;
         const CUtensorMap* m16 = is_v ? &maps.v16 : &maps.k16;
         uint64_t* full = is_v ? bars.v_full : bars.k_full;
-        uint64_t* empty = is_v ? bars.v_empty : bars.k_empty;
+        uint64_t(*taken)[2] = is_v ? bars.pv_done : bars.s_full;
         const uint32_t ring = base + (is_v ? C::OFF_V : C::OFF_K);
-        const int depth = is_v ? C::NV : C::NK;
-        int st = 0, armed = 0, q_armed = 0;
-        uint32_t phase = 1;  // of the empty barriers: the first round passes
+        int c = 0, q_armed = 0;  // tiles and items loaded
         bool ok = true;
         auto load_q = [&](const Item& it, int count) {
             const int set = count & 1;
@@ -242,7 +235,11 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         if (!is_v && !w.done(sh)) load_q(w.it, 0);
         while (ok && !w.done(sh)) {
             const int rows = rows_of(w.it, w.j), e0 = w.j * BN;
-            if (!wait_warp(&empty[st], phase, abort_, flags)) break;
+            const int st = c & 1;
+            // (the first two pass)
+            if (!wait_warp(&taken[0][st], ((c >> 1) & 1) ^ 1, abort_, flags) ||
+                !wait_warp(&taken[1][st], ((c >> 1) & 1) ^ 1, abort_, flags))
+                break;
             mbar_arrive_expect_tx_w(&full[st], rows * D * 2);
             const uint32_t dst = ring + st * C::KT;
             if (rows == BN && e0 >= w.it.pre) {
@@ -257,8 +254,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                                       w.it.b, &full[st]);
                 }
             }
-            armed++;
-            if (++st == depth) st = 0, phase ^= 1;
+            c++;
             if (!is_v && w.j == w.it.tiles - 1 && w.n + step < sh.items)
                 load_q(item_of(sh, w.n + step), w.count + 1);
             w.next(sh, step);
@@ -267,8 +263,8 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             volatile int no_abort = 0;
             for (int i = max(0, q_armed - 2); i < q_armed; i++)
                 mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
-            for (int i = max(0, armed - depth); i < armed; i++)
-                mbar_wait(&full[i % depth], (i / depth) & 1, &no_abort, flags);
+            for (int i = max(0, c - 2); i < c; i++)
+                mbar_wait(&full[i & 1], (i >> 1) & 1, &no_abort, flags);
         }
     } else if (warp == 1 || warp == 3) {
         // ----------------------------------------------- MMA issuers
@@ -278,52 +274,55 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         const uint64_t v0 = sdesc_sw128(base + C::OFF_V, BN * 128, 1024);
         constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
         const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
-        Walk a = w;                      // the tile whose logits are next; w: whose output is
-        int ca = 0, cw = 0, ka = 0, vw = 0;  // their numbers and ring stages
-        uint32_t k_phase = 0, v_phase = 0;
+        int ca = 0, cw = 0;  // tiles whose logits and whose outputs are issued
+        // of a tile, until its PV: rows / 16, and 256 if it opens its item
+        uint32_t next[2] = {0, 0};
         auto qk = [&]() {
-            if (a.j == 0 && !wait_warp(&bars.q_full[a.count & 1], (a.count >> 1) & 1, abort_, flags))
-                return false;
-            if (!wait_warp(&bars.k_full[ka], k_phase, abort_, flags)) return false;
-            fence_after_sync();
-            const uint32_t id = idesc_bf16_f32(BM, 0, false, false) |
-                                ((uint32_t)(rows_of(a.it, a.j) >> 3) << 17);
-            const uint64_t dq = q0 + ((2 * (a.count & 1) * C::QT) >> 4);
-            const uint64_t dk = k0 + ((ka * C::KT) >> 4);
+            const uint32_t rows = rows_of(w.it, w.j);
+            const uint32_t id = idesc_bf16_f32(BM, 0, false, false) | (rows >> 3 << 17);
+            const uint64_t dq = q0 + ((2 * (w.count & 1) * C::QT) >> 4);
+            const uint64_t dk = k0 + (((ca & 1) * C::KT) >> 4);
             const uint32_t d = s_col + (ca & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ks++)
                 mma_ss_w(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
                          dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
             mma_commit_w(&bars.s_full[x][ca & 1]);
-            mma_commit_w(&bars.k_empty[ka]);
-            if (a.j == a.it.tiles - 1) mma_commit_w(&bars.q_empty[a.count & 1]);
-            if (++ka == C::NK) ka = 0, k_phase ^= 1;
+            if (w.j == w.it.tiles - 1) mma_commit_w(&bars.q_empty[w.count & 1]);
+            const uint32_t info = rows >> 4 | (w.j == 0 ? 256u : 0u);
             ca++;
-            a.next(sh, step);
-            return true;
+            w.next(sh, step);
+            return info;
         };
-        auto pv = [&]() {
-            if (!wait_warp(&bars.v_full[vw], v_phase, abort_, flags)) return false;
-            if (!wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags)) return false;
+        auto ready = [&]() {  // the next tile's operands
+            return (w.j > 0 || wait_warp(&bars.q_full[w.count & 1], (w.count >> 1) & 1, abort_, flags)) &&
+                   wait_warp(&bars.k_full[ca & 1], (ca >> 1) & 1, abort_, flags);
+        };
+        bool ok = true;
+        for (int i = 0; i < 2; i++) {
+            if (w.done(sh)) break;
+            ok = ok && ready();
+            if (!ok) break;
             fence_after_sync();
-            const uint64_t dv = v0 + ((vw * C::KT) >> 4);
-            const uint32_t p = s_col + (cw & 1) * 64;
-            const int n = rows_of(w.it, w.j) >> 4;
-            mma_ts_w(o_col, p, dv, id_pv, w.j > 0);
+            next[i] = qk();
+        }
+        while (ok && cw < ca) {
+            const bool more = !w.done(sh);
+            if (!wait_warp(&bars.v_full[cw & 1], (cw >> 1) & 1, abort_, flags) || (more && !ready()) ||
+                !wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags))
+                break;
+            fence_after_sync();
+            const uint64_t dv = v0 + (((cw & 1) * C::KT) >> 4);
+            const uint32_t p = s_col + (cw & 1) * 64, n = next[0] & 255;
+            mma_ts_w(o_col, p, dv, id_pv, next[0] < 256);
 #pragma unroll
             for (int ks = 1; ks < BN / 16; ks++)
                 if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
             mma_commit_w(&bars.pv_done[x][cw & 1]);
-            mma_commit_w(&bars.v_empty[vw]);
-            if (++vw == C::NV) vw = 0, v_phase ^= 1;
+            next[0] = next[1];
+            if (more) next[1] = qk();
             cw++;
-            w.next(sh, step);
-            return true;
-        };
-        bool ok = true;
-        for (int i = 0; ok && i < 2 && !a.done(sh); i++) ok = qk();
-        while (ok && !w.done(sh)) ok = pv() && (a.done(sh) || qk());
+        }
         // every MMA issued must finish before TMEM is released
         mma_commit_w(&bars.drain[x]);
         volatile int no_abort = 0;
