@@ -137,8 +137,8 @@ struct Cfg {
     static constexpr int KT = BN * D * 2;            // a K or V tile
     static constexpr int OFF_K = 4 * QT;             // (two items of two tiles before it)
     static constexpr int OFF_V = OFF_K + 2 * KT;
-    static constexpr int OFF_O = OFF_V + 2 * KT;     // 32 rows x 32 columns per softmax warp
-    static constexpr int SMEM = OFF_O + 8 * 2048 + 1024;
+    static constexpr int OFF_O = OFF_V + 2 * KT;     // 32 rows x 64 columns per softmax warp
+    static constexpr int SMEM = OFF_O + 8 * 4096 + 1024;
     static constexpr uint32_t COL_O = 256;           // S: [tile][buffer] of 64 columns
 };
 
@@ -337,7 +337,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         int c = 0;
         // The result of an item's tile is taken while the next item's first
         // weights wait to be used: PV of its last tile is done by then.
-        uint4* stage = reinterpret_cast<uint4*>(smem + C::OFF_O + (warp - 4) * 2048);
+        uint4* stage = reinterpret_cast<uint4*>(smem + C::OFF_O + (warp - 4) * 4096);
         auto finish = [&](const Item& it, float m, float l) {
             ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1, abort_, flags));
             if (!ok) return;
@@ -349,32 +349,34 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             __nv_bfloat162 zero = __float2bfloat162_rn(l * 0.f);
             const __nv_bfloat162 nought = __float2bfloat162_rn(0.f);
             const int at = real ? (it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head : -1;
-            // through the warp's shared memory, 32 columns at a time, so that
-            // each store instruction writes whole 64-byte pieces of eight rows
+            // through the warp's shared memory, 64 columns at a time, so that
+            // each store instruction writes whole 128-byte lines of four rows
 #pragma unroll 1
-            for (int u = 0; u < D; u += 32) {
-                uint32_t r[32];
-                tmem_ld32(o_col + u, r);
+            for (int u = 0; u < D; u += 64) {
+                uint32_t r[2][32];
+                tmem_ld32(o_col + u, r[0]);
+                tmem_ld32(o_col + u + 32, r[1]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int z = 0; z < 4; z++) {
+                for (int z = 0; z < 8; z++) {
                     uint32_t p[4];
 #pragma unroll
                     for (int y = 0; y < 4; y++) {
+                        const int e = 8 * (z & 3) + 2 * y;
                         const __nv_bfloat162 v =
-                            __floats2bfloat162_rn(__uint_as_float(r[8 * z + 2 * y]) * inv,
-                                                  __uint_as_float(r[8 * z + 2 * y + 1]) * inv);
+                            __floats2bfloat162_rn(__uint_as_float(r[z >> 2][e]) * inv,
+                                                  __uint_as_float(r[z >> 2][e + 1]) * inv);
                         zero = __hfma2(v, nought, zero);
                         p[y] = *reinterpret_cast<const uint32_t*>(&v);
                     }
-                    stage[lane * 4 + ((z + (lane >> 1)) & 3)] = make_uint4(p[0], p[1], p[2], p[3]);
+                    stage[lane * 8 + (z ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
                 }
                 __syncwarp();
 #pragma unroll
-                for (int z = 0; z < 4; z++) {
-                    const int r8 = z * 8 + (lane >> 2), to = __shfl_sync(~0u, at, r8);
-                    const uint4 v = stage[r8 * 4 + (((lane & 3) + (r8 >> 1)) & 3)];
-                    if (to >= 0) *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 3) * 8) = v;
+                for (int z = 0; z < 8; z++) {
+                    const int r4 = z * 4 + (lane >> 3), to = __shfl_sync(~0u, at, r4);
+                    const uint4 v = stage[r4 * 8 + ((lane & 7) ^ (r4 & 7))];
+                    if (to >= 0) *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 7) * 8) = v;
                 }
                 __syncwarp();
             }
