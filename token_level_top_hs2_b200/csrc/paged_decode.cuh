@@ -121,7 +121,6 @@ struct Bars {
     uint64_t p_full[2];              // [group]
     uint64_t q_full[2], q_empty[2], x_full, x_empty, drain[2];
     float2 sc[kScRing];     // K and V scale of the line's pages, kAbsent for one not loaded
-    int ph[2][2][32];       // per producer and batch: its pages' (page, head) numbers, or -1
     float qf[12];           // per stage: scale log2(e) over the power of two in q's pieces
     float red[2][4][20];    // per group and warp: per-head maxima or sums, largest V scale
     float xr[16], xl[16];
@@ -143,10 +142,10 @@ constexpr uint32_t idesc_f8(int N, uint32_t bfmt, bool a_mn, bool b_mn) {
     return (1u << 4) | (bfmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
-HS2_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+HS2_DEV void mma_f8_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -242,7 +241,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ Bars bars;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = lane_id();
     volatile int* abort_ = &bars.abort_;
     const int Hkv = work.Hkv;
 
@@ -319,7 +318,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     }
     __syncthreads();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = __shfl_sync(~0u, bars.tmem, 0);
+    const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
     Walk w = {};
     if (n_tiles > 0) {
         w.b = bars.b0, w.h = bars.h0, w.t = bars.t0;
@@ -331,14 +331,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         // Warp 0 loads K, warp 3 V (and splits the items' queries: an item's
         // before its V tiles).  A lane per page: 32 pages (a batch of TPB
         // tiles) at a time, whose numbers and scales are fetched while the
-        // tiles before them are issued.  One thread issues a batch's copies
-        // from a list in shared memory: an issue takes it about 65 cycles, and
-        // 32 lanes taking turns needed twice as long for a tile.
+        // tiles before them are issued.
         constexpr int PP = kTile / PAGE, TPB = 32 / PP;
         const int is_v = warp == 3;
         const float* scale = is_v ? v_scale : k_scale;
         const CUtensorMap* map = is_v ? &map_v : &map_k;
-        uint8_t* ring = smem + (is_v ? C::OFF_V : 0);
+        const uint32_t ring = base + (is_v ? C::OFF_V : 0);
         Walk mine = w;      // where this lane's page is
         int pid = -1;
         bool want = false;
@@ -382,10 +380,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         bool ok = true;
         locate(0);
         scales();
-        for (int i0 = 0, buf = 0; ok && i0 < n_tiles; i0 += TPB, buf ^= 1) {
+        for (int i0 = 0; ok && i0 < n_tiles; i0 += TPB) {
             const int cnt = min(TPB, n_tiles - i0);
-            // the batch's list, and which of its tiles open an item
-            bars.ph[is_v][buf][lane] = ph;
+            // the batch's pages and scales, and which of its tiles open an item
+            const int ph_c = ph;
             float2* to = &bars.sc[(i0 * PP + lane) & (kScRing - 1)];
             if (is_v)
                 to->y = sc;
@@ -399,8 +397,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
             for (int s = 0; ok && s < cnt;) {
                 if (is_v && (opens >> (s * PP) & 1)) {
                     const int b = __shfl_sync(~0u, b_c, s * PP), h = __shfl_sync(~0u, h_c, s * PP);
-                    ok = __all_sync(~0u, wait(&bars.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_,
-                                                   flags));
+                    ok = wait_warp(&bars.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_, flags);
                     if (!ok) break;
                     qf = scale2 / split_q<D, NG>(q + ((size_t)b * Hkv + h) * G * D, G,
                                                  smem + C::OFF_Q + (seg & 1) * C::QB, flags);
@@ -415,32 +412,32 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     if (next) e = min(e, (__ffs(next) - 1) / PP);
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    for (int j = s; j < e; j++) {
-                        int phs[PP], n = 0;
+                for (int j = s; j < e; j++) {
+                    int phs[PP], n = 0;
 #pragma unroll
-                        for (int u = 0; u < PP; u++) phs[u] = bars.ph[is_v][buf][j * PP + u];
+                    for (int u = 0; u < PP; u++) phs[u] = __shfl_sync(~0u, ph_c, j * PP + u);
 #pragma unroll
-                        for (int u = 0; u < PP; u++) n += phs[u] >= 0;
-                        ok = wait(&bars.empty[st], ring_phase, abort_, flags);
-                        if (!ok) break;
-                        if (is_v) bars.qf[st] = qf;
-                        mbar_arrive_expect_tx(&bars.full[st], PAGE * D * n);
-#pragma unroll
-                        for (int u = 0; u < PP; u++)
-                            if (phs[u] >= 0)
-                                tma_load_3d(ring + st * C::KV + u * PAGE * D, map, 0, 0, phs[u],
-                                            &bars.full[st]);
-                        armed++;
-                        if (++st == NST) st = 0, ring_phase ^= 1;
+                    for (int u = 0; u < PP; u++) n += phs[u] >= 0;
+                    ok = wait_warp(&bars.empty[st], ring_phase, abort_, flags);
+                    if (!ok) break;
+                    if (is_v) {
+                        if (lane == 0) bars.qf[st] = qf;
+                        __syncwarp();
                     }
+                    mbar_arrive_expect_tx_w(&bars.full[st], PAGE * D * n);
+#pragma unroll
+                    for (int u = 0; u < PP; u++)
+                        if (phs[u] >= 0)
+                            tma_load_3d_w(ring + st * C::KV + u * PAGE * D, map, 0, 0, phs[u],
+                                          &bars.full[st]);
+                    armed++;
+                    if (++st == NST) st = 0, ring_phase ^= 1;
                 }
-                ok = __shfl_sync(~0u, ok, 0);
                 if (s < TPB / 2 && e >= min(cnt, TPB / 2)) scales();
                 s = e;
             }
         }
-        if (*abort_ && lane == 0) {  // let the copies in flight land before the CTA leaves
+        if (*abort_) {  // let the copies in flight land before the CTA leaves
             // (the other producer's share of a barrier may never come: the wait
             // is bounded, and by its end the copies have landed)
             volatile int no_abort = 0;
@@ -450,19 +447,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     } else if (warp == 1) {
         // ------------------------------------------------- S^T = K q^T
         constexpr uint32_t id = idesc_f8(C::NQ, 0, false, false);
-        if (lane == 0 && n_tiles > 0) {
-            const uint64_t a0 = sdesc(SWZ, smem_u32(smem), 16, ATOM);
-            const uint64_t q0 = sdesc(SWZ, smem_u32(smem + C::OFF_Q), 16, ATOM);
+        if (n_tiles > 0) {
+            const uint64_t a0 = sdesc(SWZ, base, 16, ATOM), q0 = sdesc(SWZ, base + C::OFF_Q, 16, ATOM);
             int st = 0, seg = 0;
             uint32_t ring_phase = 0;
             bool ok = true;
             for (int i = 0; ok && i < n_tiles; seg++) {
                 const int n = min(w.s.tiles - w.t, n_tiles - i);
-                ok = wait(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags);
+                ok = wait_warp(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags);
                 for (const int end = i + n; ok && i < end; i++) {
                     const int sb = (i & 1) * 2 + ((i >> 1) & 1);
-                    if (!wait(&bars.full[st], ring_phase, abort_, flags) ||
-                        !wait(&bars.s_empty[sb], ((i >> 2) & 1) ^ 1, abort_, flags)) {
+                    if (!wait_warp(&bars.full[st], ring_phase, abort_, flags) ||
+                        !wait_warp(&bars.s_empty[sb], ((i >> 2) & 1) ^ 1, abort_, flags)) {
                         ok = false;
                         break;
                     }
@@ -470,32 +466,32 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     const uint64_t a = a0 + ((st * C::KV) >> 4), bq = q0 + (((seg & 1) * C::QB) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ks++)
-                        mma_f8(tmem + sb * 32, a + ks * 2, bq + ks * 2, id, ks > 0);
-                    mma_commit(&bars.s_full[sb]);
-                    if (i + 1 == end) mma_commit(&bars.q_empty[seg & 1]);
+                        mma_f8_w(tmem + sb * 32, a + ks * 2, bq + ks * 2, id, ks > 0);
+                    mma_commit_w(&bars.s_full[sb]);
+                    if (i + 1 == end) mma_commit_w(&bars.q_empty[seg & 1]);
                     if (++st == NST) st = 0, ring_phase ^= 1;
                 }
                 w.skip(work, n, i < n_tiles);
             }
-            mma_commit(&bars.drain[0]);
+            mma_commit_w(&bars.drain[0]);
             volatile int no_abort = 0;
-            wait(&bars.drain[0], 0, &no_abort, flags);
+            mbar_wait(&bars.drain[0], 0, &no_abort, flags);
         }
     } else if (warp == 2) {
         // ----------------------------------------------- O^T += V^T w^T
         constexpr uint32_t id = idesc_f8(C::NP, 1, true, true);
-        if (lane == 0 && n_tiles > 0) {
+        if (n_tiles > 0) {
             // V: dims contiguous, eight tokens per atom; 64 dims are read twice
             // (a zero step between 64-dim blocks) for the 128 rows
-            const uint64_t a0 = sdesc(SWZ, smem_u32(smem + C::OFF_V), 0, ATOM);
-            const uint64_t p0 = sdesc(0, smem_u32(smem + C::OFF_P), 128, kTile * 16);
+            const uint64_t a0 = sdesc(SWZ, base + C::OFF_V, 0, ATOM);
+            const uint64_t p0 = sdesc(0, base + C::OFF_P, 128, kTile * 16);
             int st = 0;
             bool ok = true;
             for (int i = 0; ok && i < n_tiles;) {
                 const int n = min(w.s.tiles - w.t, n_tiles - i);
                 for (int j = 0; j < n; j++, i++) {
                     const int g = i & 1;
-                    if (!wait(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) {
+                    if (!wait_warp(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) {
                         ok = false;
                         break;
                     }
@@ -503,16 +499,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     const uint64_t a = a0 + ((st * C::KV) >> 4), bp = p0 + ((g * C::PB) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < kTile / 32; ks++)
-                        mma_f8(tmem + C::COL_O + g * 64, a + ((ks * 32 * D) >> 4),
-                               bp + ((ks * 512) >> 4), id, (j > 1 || ks > 0) ? 1u : 0u);
-                    mma_commit(&bars.empty[st]);
+                        mma_f8_w(tmem + C::COL_O + g * 64, a + ((ks * 32 * D) >> 4),
+                                 bp + ((ks * 512) >> 4), id, (j > 1 || ks > 0) ? 1u : 0u);
+                    mma_commit_w(&bars.empty[st]);
                     if (++st == NST) st = 0;
                 }
                 w.skip(work, n, i < n_tiles);
             }
-            mma_commit(&bars.drain[1]);
+            mma_commit_w(&bars.drain[1]);
             volatile int no_abort = 0;
-            wait(&bars.drain[1], 0, &no_abort, flags);
+            mbar_wait(&bars.drain[1], 0, &no_abort, flags);
         }
     } else {
         // ------------------------------------------------------ softmax
