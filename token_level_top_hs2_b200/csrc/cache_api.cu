@@ -111,6 +111,19 @@ struct PagedCall {
     unsigned* flags;
 };
 
+// The registers that the kernel's setmaxnreg splits are 512 x 128: it must have
+// been built to launch with exactly those (its warps would wait for them in vain).
+template <int D, int NG, int PAGE>
+bool registers_ok() {
+    if (NG != 16) return true;
+    static const bool ok = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, pgd::paged_decode_kernel<D, NG, PAGE>) == cudaSuccess &&
+               a.numRegs == 128;
+    }();
+    return ok;
+}
+
 template <int D, int NG>
 hs2_status run_paged(const PagedCall& c) {
     const hs2_paged_shape* s = c.s;
@@ -125,9 +138,9 @@ hs2_status run_paged(const PagedCall& c) {
     const int64_t tiles = (seen / pgd::kTile + 3) * s->Hkv * s->B;
     const int grid = (int)std::min<int64_t>(tiles, sm_count());
     if (grid < 1) return HS2_ERR_CUDA;
-    auto run = [&](auto kern) {
+    auto run = [&](auto kern, bool ok) {
         const size_t smem = pgd::Cfg<D, NG>::SMEM;
-        if (!set_smem(kern, smem)) return HS2_ERR_CUDA;
+        if (!ok || !set_smem(kern, smem)) return HS2_ERR_CUDA;
         kern<<<grid, pgd::kThreads, smem, c.st>>>(
             mk, mv, static_cast<const __nv_bfloat16*>(c.q), c.ks, c.vs, c.table, work, c.G,
             s->n_pages, s->max_pages, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.lse,
@@ -136,10 +149,10 @@ hs2_status run_paged(const PagedCall& c) {
     };
     hs2_status e;
     switch (s->page) {
-        case 16: e = run(pgd::paged_decode_kernel<D, NG, 16>); break;
-        case 32: e = run(pgd::paged_decode_kernel<D, NG, 32>); break;
-        case 64: e = run(pgd::paged_decode_kernel<D, NG, 64>); break;
-        default: e = run(pgd::paged_decode_kernel<D, NG, 128>);
+        case 16: e = run(pgd::paged_decode_kernel<D, NG, 16>, registers_ok<D, NG, 16>()); break;
+        case 32: e = run(pgd::paged_decode_kernel<D, NG, 32>, registers_ok<D, NG, 32>()); break;
+        case 64: e = run(pgd::paged_decode_kernel<D, NG, 64>, registers_ok<D, NG, 64>()); break;
+        default: e = run(pgd::paged_decode_kernel<D, NG, 128>, registers_ok<D, NG, 128>());
     }
     if (e != HS2_OK) return e;
     return launch_pdl(pgd::paged_merge_kernel<D>, dim3(s->Hkv * c.G, s->B), dim3(D), 0, c.st, work, c.G,

@@ -29,7 +29,7 @@ using namespace hs2::tc;
 using kvc::e4m3x2;
 
 constexpr int kTile = 128;       // tokens per tile
-constexpr int kThreads = 384;    // K, QK, PV, V warps and two softmax groups of four
+constexpr int kThreads = 512;    // QK, PV, q, -; four producers; two softmax groups of four
 constexpr int kMaxCtas = 148;    // one per SM
 constexpr float kTopLog2 = 11.f;    // a raised reference maps the largest weight to 2^11
 constexpr float kHalfStep = 7.62939453125e-6f;  // 2^-17, half of e5m2's smallest step
@@ -121,10 +121,11 @@ struct Bars {
     uint64_t p_full[2];              // [group]
     uint64_t q_full[2], q_empty[2], x_full, x_empty, drain[2];
     float2 sc[kScRing];     // K and V scale of the line's pages, kAbsent for one not loaded
-    float qf[12];           // per stage: scale log2(e) over the power of two in q's pieces
+    float qf[2];            // per item & 1: scale log2(e) over the power of two in q's pieces
+    float sqf[4];           // the same per logit buffer
     float red[2][4][20];    // per group and warp: per-head maxima or sums, largest V scale
     float xr[16], xl[16];
-    unsigned long long total;
+    int64_t total;
     int b0, h0, t0;
     uint32_t tmem;
     int abort_;
@@ -251,7 +252,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 4; i++) {
-            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_full[i], 2);   // the MMAs, and the warp that issues them
             mbar_init(&bars.s_empty[i], 4);
         }
         for (int i = 0; i < 2; i++) {
@@ -263,8 +264,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         mbar_init(&bars.x_full, 4);
         mbar_init(&bars.x_empty, 4);
         bars.abort_ = 0;
-        bars.total = 0;
-        bars.b0 = bars.h0 = bars.t0 = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -272,52 +271,54 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         tmem_relinquish();
     }
     griddep_launch();
-    if (warp == 0 && lane == 0) {
+    if (warp == 4) {
         tma_prefetch_map(&map_k);
         tma_prefetch_map(&map_v);
+    }
+    if (warp == 2) {
+        // the length of the whole line of tiles, and the item that the CTA starts in
+        const int cta = blockIdx.x;
+        bool bad = false;
+        int64_t sum = 0;
+#pragma unroll 4
+        for (int b = lane; b < work.B; b += 32)
+            sum += span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
+        if (bad && cta == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(~0u, sum, off);
+        const int64_t total = sum * Hkv;
+        const int n = (int)min((int64_t)gridDim.x, total);
+        if (lane == 0) bars.total = total, bars.b0 = bars.h0 = bars.t0 = 0;
+        __syncwarp();
+        if (cta < n) {
+            const int64_t first = cut(total, cta, n);
+            int64_t before = 0;
+            for (int b = 0; b < work.B && before * Hkv <= first; b += 32) {
+                const int nt = b + lane < work.B ? span_of(length_of(work.lengths, b + lane, work.cap, &bad),
+                                                           work.window, work.n_sink).tiles
+                                                 : 0;
+                int64_t upto = nt;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int64_t u = __shfl_up_sync(~0u, upto, off);
+                    if (lane >= off) upto += u;
+                }
+                const int64_t at = first - (before + upto - nt) * Hkv;
+                if (at >= 0 && at < (int64_t)nt * Hkv) {
+                    bars.b0 = b + lane;
+                    bars.h0 = (int)(at / nt);
+                    bars.t0 = (int)(at % nt);
+                }
+                before += __shfl_sync(~0u, upto, 31);
+            }
+        }
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    // the length of the whole line of tiles
-    {
-        unsigned long long n = 0;
-        bool bad = false;
-        for (int b = tid; b < work.B; b += kThreads)
-            n += span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
-        if (n) atomicAdd(&bars.total, n);
-        if (bad && blockIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
-    }
-    __syncthreads();
-    const int64_t total = (int64_t)bars.total * Hkv;
+    const int64_t total = bars.total;
     const int n_cta = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-    const int64_t g0 = cta < n_cta ? cut(total, cta, n_cta) : 0;
-    const int n_tiles = cta < n_cta ? (int)(cut(total, cta + 1, n_cta) - g0) : 0;
-    if (n_tiles > 0 && warp == 0) {
-        // the item that the CTA starts in
-        int64_t before = 0;
-        for (int b = 0; b < work.B; b += 32) {
-            bool bad = false;
-            const int nt = b + lane < work.B ? span_of(length_of(work.lengths, b + lane, work.cap, &bad),
-                                                  work.window, work.n_sink).tiles
-                                        : 0;
-            int64_t sum = nt;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t u = __shfl_up_sync(~0u, sum, off);
-                if (lane >= off) sum += u;
-            }
-            const int64_t at = g0 - (before + sum - nt) * Hkv;
-            if (at >= 0 && at < (int64_t)nt * Hkv) {
-                bars.b0 = b + lane;
-                bars.h0 = (int)(at / nt);
-                bars.t0 = (int)(at % nt);
-            }
-            before += __shfl_sync(~0u, sum, 31);
-            if (before * Hkv > g0) break;
-        }
-    }
-    __syncthreads();
+    const int n_tiles = cta < n_cta ? (int)(cut(total, cta + 1, n_cta) - cut(total, cta, n_cta)) : 0;
     const uint32_t tmem = __shfl_sync(~0u, bars.tmem, 0);
     const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
     Walk w = {};
@@ -326,93 +327,81 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         w.load(work);
     }
 
-    if (warp == 0 || warp == 3) {
-        // ------------------------------------------------------ producers
-        // Warp 0 loads K, warp 3 V (and splits the items' queries: an item's
-        // before its V tiles).  A lane per page: 32 pages (a batch of TPB
-        // tiles) at a time, whose numbers and scales are fetched while the
-        // tiles before them are issued.
-        constexpr int PP = kTile / PAGE, TPB = 32 / PP;
-        const int is_v = warp == 3;
-        const float* scale = is_v ? v_scale : k_scale;
-        const CUtensorMap* map = is_v ? &map_v : &map_k;
-        const uint32_t ring = base + (is_v ? C::OFF_V : 0);
-        Walk mine = w;      // where this lane's page is
-        int pid = -1;
-        bool want = false;
-        float sc = 0.f;
-        int ph = -1;
-        // this lane's page of the tiles i0 .. i0 + TPB - 1, and its number
-        auto locate = [&](int i0) {
-            mine = w;
-            int left = min(lane / PP, n_tiles - 1 - i0);  // tiles on from i0's
-            while (left > 0 && mine.t + left >= mine.s.tiles) {
-                const int n = mine.s.tiles - mine.t;
-                left -= n;
-                mine.skip(work, n, true);
-            }
-            mine.t += max(left, 0);
-            const int p = mine.tile() * PP + lane % PP, pos = p * PAGE;
-            want = i0 + lane / PP < n_tiles && pos < mine.s.T &&
-                   (pos + PAGE > mine.s.w0 || pos < mine.s.ns);
-            pid = want ? __ldg(table + (size_t)mine.b * max_pages + p) : -1;
-        };
-        // the first tile of the batch behind: one on from lane 31's
-        auto move_on = [&](int i0) {
-            if (i0 + TPB >= n_tiles) return;
-            w.b = __shfl_sync(~0u, mine.b, 31);
-            w.h = __shfl_sync(~0u, mine.h, 31);
-            w.t = __shfl_sync(~0u, mine.t, 31);
-            w.load(work);
-            w.skip(work, 1, true);
-        };
-        auto scales = [&]() {
-            if (want && (pid < 0 || pid >= n_pages)) {
-                atomicOr(flags, FLAG_BAD_INDEX);
-                want = false;
-            }
-            ph = want ? pid * Hkv + mine.h : -1;
-            sc = want ? __ldg(scale + ph) : kAbsent;
-        };
-        int armed = 0, seg = 0, st = 0;
-        uint32_t ring_phase = 1;  // of the empty barriers: the first round passes
-        float qf = 0.f;
-        bool ok = true;
-        locate(0);
-        scales();
-        for (int i0 = 0; ok && i0 < n_tiles; i0 += TPB) {
-            const int cnt = min(TPB, n_tiles - i0);
-            // the batch's pages and scales, and which of its tiles open an item
-            const int ph_c = ph;
-            float2* to = &bars.sc[(i0 * PP + lane) & (kScRing - 1)];
-            if (is_v)
-                to->y = sc;
-            else
-                to->x = sc;
-            const int b_c = mine.b, h_c = mine.h;
-            const uint32_t opens = __ballot_sync(
-                ~0u, lane % PP == 0 && lane / PP < cnt && (mine.t == 0 || (i0 == 0 && lane == 0)));
-            move_on(i0);
-            locate(i0 + TPB);  // (their numbers arrive during the first half)
-            for (int s = 0; ok && s < cnt;) {
-                if (is_v && (opens >> (s * PP) & 1)) {
-                    const int b = __shfl_sync(~0u, b_c, s * PP), h = __shfl_sync(~0u, h_c, s * PP);
-                    ok = wait_warp(&bars.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_, flags);
-                    if (!ok) break;
-                    qf = scale2 / split_q<D, NG>(q + ((size_t)b * Hkv + h) * G * D, G,
-                                                 smem + C::OFF_Q + (seg & 1) * C::QB, flags);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.q_full[seg & 1]);
-                    seg++;
+    // (16 heads' softmax needs more registers than 512 threads get at launch;
+    // the 65,536 are 512 x 128 = 256 x 80 + 256 x 176)
+    if (warp < 8) {
+        if constexpr (NG == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp >= 4) {
+            // ------------------------------------------------------ producers
+            // Warps 4 and 6 load K, 5 and 7 V, of every other tile: a warp's
+            // copies move at most 14 bytes per cycle whatever their size (its
+            // scheduler's share of the copy engine), two warps' 24 to 28, four
+            // warps' what the memory gives, 30 to 33.
+            // A lane per page: 32 pages (a batch of TPB of the warp's tiles) at a
+            // time, whose numbers and scales are fetched while the tiles before
+            // them are issued.
+            constexpr int PP = kTile / PAGE, TPB = 32 / PP;
+            constexpr int EVERY = D == 128 ? 1 : 2;
+            const int is_v = warp & 1, odd = (warp >> 1) & 1;
+            // the warp's tiles: odd, odd + EVERY, ...
+            const int n_own = odd < EVERY ? (n_tiles + EVERY - 1 - odd) / EVERY : 0;
+            if (odd && n_own > 0) w.skip(work, 1, true);
+            const float* scale = is_v ? v_scale : k_scale;
+            const CUtensorMap* map = is_v ? &map_v : &map_k;
+            const uint32_t ring = base + (is_v ? C::OFF_V : 0);
+            Walk mine = w;      // where this lane's page is
+            int pid = -1;
+            bool want = false;
+            float sc = 0.f;
+            int ph = -1;
+            // this lane's page of the warp's tiles i0 .. i0 + TPB - 1, and its number
+            auto locate = [&](int i0) {
+                mine = w;
+                int left = EVERY * min(lane / PP, n_own - 1 - i0);  // tiles on from i0's
+                while (left > 0 && mine.t + left >= mine.s.tiles) {
+                    const int n = mine.s.tiles - mine.t;
+                    left -= n;
+                    mine.skip(work, n, true);
                 }
-                int e = s < TPB / 2 ? min(cnt, TPB / 2) : cnt;
-                if (is_v) {
-                    const uint32_t next = opens & ~((2u << (s * PP)) - 1);  // (s * PP < 32)
-                    if (next) e = min(e, (__ffs(next) - 1) / PP);
+                mine.t += max(left, 0);
+                const int p = mine.tile() * PP + lane % PP, pos = p * PAGE;
+                want = i0 + lane / PP < n_own && pos < mine.s.T &&
+                       (pos + PAGE > mine.s.w0 || pos < mine.s.ns);
+                pid = want ? __ldg(table + (size_t)mine.b * max_pages + p) : -1;
+            };
+            // the first tile of the batch behind lane 31's
+            auto move_on = [&](int i0) {
+                if (i0 + TPB >= n_own) return;
+                w.b = __shfl_sync(~0u, mine.b, 31);
+                w.h = __shfl_sync(~0u, mine.h, 31);
+                w.t = __shfl_sync(~0u, mine.t, 31);
+                w.load(work);
+                for (int u = 0; u < EVERY; u++) w.skip(work, 1, true);
+            };
+            auto scales = [&]() {
+                if (want && (pid < 0 || pid >= n_pages)) {
+                    atomicOr(flags, FLAG_BAD_INDEX);
+                    want = false;
                 }
+                ph = want ? pid * Hkv + mine.h : -1;
+                sc = want ? __ldg(scale + ph) : kAbsent;
+            };
+            int armed = 0, st = odd;
+            uint32_t ring_phase = 1;  // of the empty barriers: the first round passes
+            bool ok = true;
+            locate(0);
+            scales();
+            for (int i0 = 0; ok && i0 < n_own; i0 += TPB) {
+                const int cnt = min(TPB, n_own - i0), ph_c = ph;
+                float2* to = &bars.sc[((EVERY * (i0 + lane / PP) + odd) * PP + lane % PP) & (kScRing - 1)];
+                if (is_v)
+                    to->y = sc;
+                else
+                    to->x = sc;
                 __syncwarp();
-                for (int j = s; j < e; j++) {
+                move_on(i0);
+                locate(i0 + TPB);  // (their numbers arrive during the first half)
+                for (int j = 0; j < cnt; j++) {
                     int phs[PP], n = 0;
 #pragma unroll
                     for (int u = 0; u < PP; u++) phs[u] = __shfl_sync(~0u, ph_c, j * PP + u);
@@ -420,103 +409,124 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     for (int u = 0; u < PP; u++) n += phs[u] >= 0;
                     ok = wait_warp(&bars.empty[st], ring_phase, abort_, flags);
                     if (!ok) break;
-                    if (is_v) {
-                        if (lane == 0) bars.qf[st] = qf;
-                        __syncwarp();
-                    }
                     mbar_arrive_expect_tx_w(&bars.full[st], PAGE * D * n);
 #pragma unroll
                     for (int u = 0; u < PP; u++)
                         if (phs[u] >= 0)
-                            tma_load_3d_w(ring + st * C::KV + u * PAGE * D, map, 0, 0, phs[u],
-                                          &bars.full[st]);
+                            tma_load_3d_w(ring + st * C::KV + u * PAGE * D, map, 0, 0, phs[u], &bars.full[st]);
                     armed++;
-                    if (++st == NST) st = 0, ring_phase ^= 1;
+                    st += EVERY;
+                    if (st >= NST) st -= NST, ring_phase ^= 1;
+                    if (j == (cnt - 1) / 2) scales();
                 }
-                if (s < TPB / 2 && e >= min(cnt, TPB / 2)) scales();
-                s = e;
             }
-        }
-        if (*abort_) {  // let the copies in flight land before the CTA leaves
-            // (the other producer's share of a barrier may never come: the wait
-            // is bounded, and by its end the copies have landed)
-            volatile int no_abort = 0;
-            for (int i = max(0, armed - NST); i < armed; i++)
-                wait(&bars.full[i % NST], (i / NST) & 1, &no_abort, flags);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------- S^T = K q^T
-        constexpr uint32_t id = idesc_f8(C::NQ, 0, false, false);
-        if (n_tiles > 0) {
-            const uint64_t a0 = sdesc(SWZ, base, 16, ATOM), q0 = sdesc(SWZ, base + C::OFF_Q, 16, ATOM);
-            int st = 0, seg = 0;
-            uint32_t ring_phase = 0;
+            if (*abort_) {  // let the copies in flight land before the CTA leaves
+                // (the other producer's share of a barrier may never come: the wait
+                // is bounded, and by its end the copies have landed)
+                volatile int no_abort = 0;
+                for (int j = max(0, armed - NST / EVERY); j < armed; j++)
+                    mbar_wait(&bars.full[(EVERY * j + odd) % NST], ((EVERY * j + odd) / NST) & 1, &no_abort,
+                              flags);
+            }
+        } else if (warp == 0) {
+            // ------------------------------------------------- S^T = K q^T
+            constexpr uint32_t id = idesc_f8(C::NQ, 0, false, false);
+            if (n_tiles > 0) {
+                const uint64_t a0 = sdesc(SWZ, base, 16, ATOM), q0 = sdesc(SWZ, base + C::OFF_Q, 16, ATOM);
+                int st = 0, seg = 0;
+                uint32_t ring_phase = 0;
+                bool ok = true;
+                for (int i = 0; ok && i < n_tiles; seg++) {
+                    const int n = min(w.s.tiles - w.t, n_tiles - i);
+                    ok = wait_warp(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags);
+                    const float qf = bars.qf[seg & 1];
+                    for (const int end = i + n; ok && i < end; i++) {
+                        const int sb = (i & 1) * 2 + ((i >> 1) & 1);
+                        if (!wait_warp(&bars.full[st], ring_phase, abort_, flags) ||
+                            !wait_warp(&bars.s_empty[sb], ((i >> 2) & 1) ^ 1, abort_, flags)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after_sync();
+                        const uint64_t a = a0 + ((st * C::KV) >> 4), bq = q0 + (((seg & 1) * C::QB) >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < D / 32; ks++)
+                            mma_f8_w(tmem + sb * 32, a + ks * 2, bq + ks * 2, id, ks > 0);
+                        mma_commit_w(&bars.s_full[sb]);
+                        if (i + 1 == end) mma_commit_w(&bars.q_empty[seg & 1]);
+                        if (lane == 0) {
+                            bars.sqf[sb] = qf;
+                            mbar_arrive(&bars.s_full[sb]);
+                        }
+                        __syncwarp();
+                        if (++st == NST) st = 0, ring_phase ^= 1;
+                    }
+                    w.skip(work, n, i < n_tiles);
+                }
+                mma_commit_w(&bars.drain[0]);
+                volatile int no_abort = 0;
+                mbar_wait(&bars.drain[0], 0, &no_abort, flags);
+            }
+        } else if (warp == 1) {
+            // ----------------------------------------------- O^T += V^T w^T
+            constexpr uint32_t id = idesc_f8(C::NP, 1, true, true);
+            if (n_tiles > 0) {
+                // V: dims contiguous, eight tokens per atom; 64 dims are read twice
+                // (a zero step between 64-dim blocks) for the 128 rows
+                const uint64_t a0 = sdesc(SWZ, base + C::OFF_V, 0, ATOM);
+                const uint64_t p0 = sdesc(0, base + C::OFF_P, 128, kTile * 16);
+                int st = 0;
+                bool ok = true;
+                for (int i = 0; ok && i < n_tiles;) {
+                    const int n = min(w.s.tiles - w.t, n_tiles - i);
+                    for (int j = 0; j < n; j++, i++) {
+                        const int g = i & 1;
+                        if (!wait_warp(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after_sync();
+                        const uint64_t a = a0 + ((st * C::KV) >> 4), bp = p0 + ((g * C::PB) >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < kTile / 32; ks++)
+                            mma_f8_w(tmem + C::COL_O + g * 64, a + ((ks * 32 * D) >> 4),
+                                     bp + ((ks * 512) >> 4), id, (j > 1 || ks > 0) ? 1u : 0u);
+                        mma_commit_w(&bars.empty[st]);
+                        if (++st == NST) st = 0;
+                    }
+                    w.skip(work, n, i < n_tiles);
+                }
+                mma_commit_w(&bars.drain[1]);
+                volatile int no_abort = 0;
+                mbar_wait(&bars.drain[1], 0, &no_abort, flags);
+            }
+        } else if (warp == 2) {
+            // --------------------------------------------------- q's pieces
             bool ok = true;
+            int seg = 0;
             for (int i = 0; ok && i < n_tiles; seg++) {
+                ok = wait_warp(&bars.q_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort_, flags);
+                if (!ok) break;
+                const float f = split_q<D, NG>(q + ((size_t)w.b * Hkv + w.h) * G * D, G,
+                                               smem + C::OFF_Q + (seg & 1) * C::QB, flags);
+                if (lane == 0) bars.qf[seg & 1] = scale2 / f;
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_full[seg & 1]);
                 const int n = min(w.s.tiles - w.t, n_tiles - i);
-                ok = wait_warp(&bars.q_full[seg & 1], (seg >> 1) & 1, abort_, flags);
-                for (const int end = i + n; ok && i < end; i++) {
-                    const int sb = (i & 1) * 2 + ((i >> 1) & 1);
-                    if (!wait_warp(&bars.full[st], ring_phase, abort_, flags) ||
-                        !wait_warp(&bars.s_empty[sb], ((i >> 2) & 1) ^ 1, abort_, flags)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after_sync();
-                    const uint64_t a = a0 + ((st * C::KV) >> 4), bq = q0 + (((seg & 1) * C::QB) >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < D / 32; ks++)
-                        mma_f8_w(tmem + sb * 32, a + ks * 2, bq + ks * 2, id, ks > 0);
-                    mma_commit_w(&bars.s_full[sb]);
-                    if (i + 1 == end) mma_commit_w(&bars.q_empty[seg & 1]);
-                    if (++st == NST) st = 0, ring_phase ^= 1;
-                }
+                i += n;
                 w.skip(work, n, i < n_tiles);
             }
-            mma_commit_w(&bars.drain[0]);
-            volatile int no_abort = 0;
-            mbar_wait(&bars.drain[0], 0, &no_abort, flags);
-        }
-    } else if (warp == 2) {
-        // ----------------------------------------------- O^T += V^T w^T
-        constexpr uint32_t id = idesc_f8(C::NP, 1, true, true);
-        if (n_tiles > 0) {
-            // V: dims contiguous, eight tokens per atom; 64 dims are read twice
-            // (a zero step between 64-dim blocks) for the 128 rows
-            const uint64_t a0 = sdesc(SWZ, base + C::OFF_V, 0, ATOM);
-            const uint64_t p0 = sdesc(0, base + C::OFF_P, 128, kTile * 16);
-            int st = 0;
-            bool ok = true;
-            for (int i = 0; ok && i < n_tiles;) {
-                const int n = min(w.s.tiles - w.t, n_tiles - i);
-                for (int j = 0; j < n; j++, i++) {
-                    const int g = i & 1;
-                    if (!wait_warp(&bars.p_full[g], (i >> 1) & 1, abort_, flags)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after_sync();
-                    const uint64_t a = a0 + ((st * C::KV) >> 4), bp = p0 + ((g * C::PB) >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < kTile / 32; ks++)
-                        mma_f8_w(tmem + C::COL_O + g * 64, a + ((ks * 32 * D) >> 4),
-                                 bp + ((ks * 512) >> 4), id, (j > 1 || ks > 0) ? 1u : 0u);
-                    mma_commit_w(&bars.empty[st]);
-                    if (++st == NST) st = 0;
-                }
-                w.skip(work, n, i < n_tiles);
-            }
-            mma_commit_w(&bars.drain[1]);
-            volatile int no_abort = 0;
-            mbar_wait(&bars.drain[1], 0, &no_abort, flags);
         }
     } else {
+        // (waits in line: a call would keep the compiler from the extra registers)
+        if constexpr (NG == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // ------------------------------------------------------ softmax
         // Two groups of four warps take the tiles in turn, each with its own
         // reference, sums and accumulator.  thread = token = TMEM lane of S^T,
         // and = dim = TMEM lane of O^T.  A wait that gives up clears ok; the
         // group leaves together at its next meeting (group_any).
-        const int g = (warp >> 2) - 1, wq = warp & 3, row = wq * 32 + lane;
+        const int g = (warp >> 2) - 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + g * 64;
         float R[NG], l[NG], vref = 0.f, vinv = 0.f;
@@ -538,13 +548,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 const int t = w.t + j;
                 const int s = (t < w.s.sink_tiles ? t : w.s.first + t - w.s.sink_tiles) * kTile + row;
                 // the tile's copies have landed: its scales are there
-                ok = ok && wait(&bars.full[st], ph, abort_, flags);
+                ok = ok && mbar_wait(&bars.full[st], ph, abort_, flags);
                 const float2 sc = bars.sc[((i0 + j) * (kTile / PAGE) + row / PAGE) & (kScRing - 1)];
                 const bool vis = s < w.s.T && (s >= w.s.w0 || s < w.s.ns) && sc.x != kAbsent;
-                const float f = vis ? sc.x * bars.qf[st] : 0.f;
                 const float sv = vis ? sc.y : 0.f;
-                ok = ok && wait(&bars.s_full[sb], (k >> 1) & 1, abort_, flags);
+                ok = ok && mbar_wait(&bars.s_full[sb], (k >> 1) & 1, abort_, flags);
                 fence_after_sync();
+                const float f = vis ? sc.x * bars.sqf[sb] : 0.f;
                 uint32_t r[C::NQ];
                 tmem_ldn<C::NQ>(lanes + sb * 32, r);
                 tmem_ld_wait();
@@ -561,7 +571,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 const bool raise = vis && (!has || top > kRaiseLog2 || sv > 2.f * vref);
                 if (group_any(g, raise || !ok)) {
                     // a new reference (the segment's first tile, or a larger weight)
-                    if (j > 1) ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
+                    if (j > 1) ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
                     fence_after_sync();
 #pragma unroll
                     for (int h = 0; h < NG; h++) {
@@ -640,7 +650,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     x0 = rest(x0), x1 = rest(x1);
                     b3[j] = prmt(x0, x1, 0x7531u);
                 }
-                if (k > 0) ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
+                if (k > 0) ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
                 uint8_t* p = smem + C::OFF_P + g * C::PB + row * 16;
                 if constexpr (NG == 16) {
                     *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
@@ -668,7 +678,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
             const bool item_end = w.t + n == w.s.tiles;
             if (mine > 0) {
                 // ------------------------------------ the segment's result
-                ok = ok && wait(&bars.empty[st_was], ph_was, abort_, flags);
+                ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
                 fence_after_sync();
                 // sums over the warp's lanes: each step halves the heads a lane holds
 #pragma unroll
@@ -722,7 +732,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 if (both && g == 1) {
                     // hand the result to group 0
                     if (n_x > 0)
-                        ok = ok && wait(&bars.x_empty, (n_x - 1) & 1, abort_, flags);
+                        ok = ok && mbar_wait(&bars.x_empty, (n_x - 1) & 1, abort_, flags);
                     if (row < D)
 #pragma unroll
                         for (int h = 0; h < NG; h++) xo[h * D + row] = O[h];
@@ -733,7 +743,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     if (lane == 0) mbar_arrive(&bars.x_full);
                 } else {
                     if (both) {
-                        ok = ok && wait(&bars.x_full, n_x & 1, abort_, flags);
+                        ok = ok && mbar_wait(&bars.x_full, n_x & 1, abort_, flags);
 #pragma unroll
                         for (int h = 0; h < NG; h++) {
                             const float xr = bars.xr[h], M = fmaxf(R[h], xr);
