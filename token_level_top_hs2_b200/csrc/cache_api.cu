@@ -205,10 +205,10 @@ hs2_status hs2_kv_write(const hs2_cache_shape* shape, int N, const void* k_new, 
     unsigned* flags = device_flags();
     if (!flags) return HS2_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int rows = 256 / (shape->d / 8) * kvc::kTokRows;
+    const int rows = kvc::kThreads / (shape->d / 8) * kvc::kRows;
     const dim3 grid((N + rows - 1) / rows, shape->B);
     auto run = [&](auto kern) {
-        kern<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(k_new),
+        kern<<<grid, kvc::kThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(k_new),
                                    static_cast<const __nv_bfloat16*>(v_new), start, count,
                                    static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
                                    k_scale, v_scale, N, shape->Tmax, flags);
@@ -228,10 +228,10 @@ hs2_status hs2_kv_read(const hs2_cache_shape* shape, int N, const void* k_cache,
     unsigned* flags = device_flags();
     if (!flags) return HS2_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int rows = 256 / (shape->d / 16);
+    const int rows = kvc::kThreads / (shape->d / 8) * kvc::kRows;
     const dim3 grid((N + rows - 1) / rows, shape->B);
     auto run = [&](auto kern) {
-        kern<<<grid, 256, 0, st>>>(static_cast<const uint8_t*>(k_cache),
+        kern<<<grid, kvc::kThreads, 0, st>>>(static_cast<const uint8_t*>(k_cache),
                                    static_cast<const uint8_t*>(v_cache), k_scale, v_scale, start,
                                    count, static_cast<__nv_bfloat16*>(k),
                                    static_cast<__nv_bfloat16*>(v), N, shape->Tmax, flags);
@@ -272,14 +272,14 @@ hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_
     unsigned* flags = device_flags();
     if (!flags) return HS2_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t blocks = ((int64_t)N * shape->Hkv * (shape->d / 16) + 255) / 256;
-    if (blocks > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    const int rows = kvc::kThreads / (shape->d / 8) * kvc::kPagedRows;
+    int log_page = 0;
+    while (1 << log_page < shape->page) log_page++;
     auto run = [&](auto kern) {
-        kern<<<dim3((unsigned)blocks, shape->B), 256, 0, st>>>(
+        kern<<<dim3((N + rows - 1) / rows, shape->B, shape->Hkv), kvc::kThreads, 0, st>>>(
             static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(v_pages), k_scale,
             v_scale, table, start, count, static_cast<__nv_bfloat16*>(k),
-            static_cast<__nv_bfloat16*>(v), N, shape->Hkv, shape->page, shape->n_pages,
-            shape->max_pages, flags);
+            static_cast<__nv_bfloat16*>(v), N, log_page, shape->n_pages, shape->max_pages, flags);
         return launch_status();
     };
     return shape->d == 128 ? run(kvc::paged_read_kernel<128>) : run(kvc::paged_read_kernel<64>);

@@ -60,83 +60,114 @@ HS2_DEV float page_scale(float top) {
 }
 
 // ------------------------------------------------------------- token cache
-// One group of D/8 lanes per row, eight elements a lane; each group takes the
-// K and the V row of kRows tokens, all loads in flight together.
-constexpr int kTokRows = 2;
+constexpr int kThreads = 256;
+constexpr int kRows = 2;  // rows of K and of V that a thread has in flight
 
+// Eight elements of a row over its scale, as e4m3 codes of the fp32 quotients.
+// A division's ten instructions each took two thirds of this kernel's time
+// (128k rows in 28.7 us), so the quotient is formed by Markstein's method
+// (IBM J. Res. Dev. 34, 1990): with r = 1 / s rounded to nearest and q = x r,
+// the fused q + r (x - q s) is x / s rounded to nearest.  It needs the exact
+// remainder to be representable; below s = 2^-60, and with infinities among
+// the elements, they are divided.
+HS2_DEV uint2 quantise8(uint4 w, float s, float r, bool finite) {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        y[2 * i] = bf16_lo(in[i]);
+        y[2 * i + 1] = bf16_hi(in[i]);
+    }
+    if (s >= 8.67361738e-19f && finite) {  // 2^-60
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float q = y[i] * r;
+            y[i] = fmaf(fmaf(-q, s, y[i]), r, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[i] = y[i] / s;
+    }
+    return make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16,
+                      e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
+}
+
+// One group of D/8 lanes per row, eight elements a lane.  grid (rows, B).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 token_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
                    const int32_t* __restrict__ start, const int32_t* __restrict__ count,
                    uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
                    float* __restrict__ k_scale, float* __restrict__ v_scale, int N, int Tmax,
                    unsigned* __restrict__ flags) {
-    constexpr int LPR = D / 8;         // lanes per row
-    constexpr int RPB = 256 / LPR;     // rows per block and step
+    constexpr int LPR = D / 8;              // lanes per row
+    constexpr int RPB = kThreads / LPR;     // rows per block and step
     const int b = blockIdx.y;
     const int lane = threadIdx.x % LPR;
     const int s0 = start[b], n = count ? count[b] : N;
-    if (n < 0 || n > N || s0 < 0 || s0 > Tmax - n) {
+    const bool in_range = n >= 0 && n <= N && s0 >= 0 && s0 <= Tmax - n;
+    const int i0 = blockIdx.x * (RPB * kRows) + threadIdx.x / LPR;
+    uint4 w[2 * kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const int i = i0 + r * RPB;
+        const size_t src = ((size_t)b * N + i) * D + lane * 8;
+        w[2 * r] = i < N ? ldg_stream(k_new + src) : make_uint4(0, 0, 0, 0);
+        w[2 * r + 1] = i < N ? ldg_stream(v_new + src) : make_uint4(0, 0, 0, 0);
+    }
+    if (!in_range) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
         return;
     }
-    const int i0 = blockIdx.x * (RPB * kTokRows) + threadIdx.x / LPR;
-    uint4 w[2 * kTokRows];
-#pragma unroll
-    for (int r = 0; r < kTokRows; r++) {
-        const int i = i0 + r * RPB;
-        const size_t src = ((size_t)b * N + i) * D + lane * 8;
-        w[2 * r] = i < n ? ldg_stream(k_new + src) : make_uint4(0, 0, 0, 0);
-        w[2 * r + 1] = i < n ? ldg_stream(v_new + src) : make_uint4(0, 0, 0, 0);
-    }
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 2 * kTokRows; j++) {
+    for (int j = 0; j < 2 * kRows; j++) {
         const int i = i0 + (j >> 1) * RPB;
-        uint32_t top = amax_bits(w[j], &bad);
+        bool odd = false;
+        uint32_t top = amax_bits(w[j], &odd);
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
         const float s = top ? __uint_as_float(top << 16) / kE4m3Max : 1.f;
-        const uint32_t c0 = e4m3x2(bf16_lo(w[j].x) / s, bf16_hi(w[j].x) / s);
-        const uint32_t c1 = e4m3x2(bf16_lo(w[j].y) / s, bf16_hi(w[j].y) / s);
-        const uint32_t c2 = e4m3x2(bf16_lo(w[j].z) / s, bf16_hi(w[j].z) / s);
-        const uint32_t c3 = e4m3x2(bf16_lo(w[j].w) / s, bf16_hi(w[j].w) / s);
         if (i < n) {
+            const uint2 c = quantise8(w[j], s, 1.f / s, !odd);
             const size_t row = (size_t)b * Tmax + s0 + i;
-            *reinterpret_cast<uint2*>((j & 1 ? v_cache : k_cache) + row * D + lane * 8) =
-                make_uint2(c0 | c1 << 16, c2 | c3 << 16);
+            *reinterpret_cast<uint2*>((j & 1 ? v_cache : k_cache) + row * D + lane * 8) = c;
             if (lane == 0) (j & 1 ? v_scale : k_scale)[row] = s;
+            bad |= odd;
         }
     }
     if (bad) atomicOr(flags, FLAG_NONFINITE);
 }
 
-// Sixteen codes and their scale -> sixteen bf16 (rounded to nearest even once:
-// code and scale multiply exactly enough in fp32, whose rounding of the
-// product is 2^-24 relative, far below bf16's).
-HS2_DEV void dequant16(uint4 c, float s, uint4& lo, uint4& hi) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8];
+// Eight codes and their scale -> eight bf16 (rounded to nearest even: fp32's
+// rounding of the product is 2^-24 relative, far below bf16's).
+HS2_DEV uint4 dequant8(uint2 c, float s) {
+    const uint32_t w[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
+    uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const float2 a = f16x2_to_float2(e4m3x2_lo_to_f16x2(w[i]));
-        const float2 b = f16x2_to_float2(e4m3x2_lo_to_f16x2(w[i] >> 16));
-        r[2 * i] = pack_bf16(a.x * s, a.y * s);
-        r[2 * i + 1] = pack_bf16(b.x * s, b.y * s);
+        r[i] = pack_bf16(a.x * s, a.y * s);
     }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+HS2_DEV uint2 ldg_stream8(const void* p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
 }
 
+// Eight codes a lane, so that a warp's stores are whole 512-byte runs.
+// grid (rows, B).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 token_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                   const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                   const int32_t* __restrict__ start, const int32_t* __restrict__ count,
                   __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v, int N, int Tmax,
                   unsigned* __restrict__ flags) {
-    constexpr int LPR = D / 16;
-    constexpr int RPB = 256 / LPR;
+    constexpr int LPR = D / 8;
+    constexpr int RPB = kThreads / LPR;
     const int b = blockIdx.y;
     const int lane = threadIdx.x % LPR;
     const int s0 = start[b], n = count ? count[b] : N;
@@ -144,20 +175,26 @@ token_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
         return;
     }
-    const int i = blockIdx.x * RPB + threadIdx.x / LPR;
-    if (i >= n) return;
-    const size_t row = (size_t)b * Tmax + s0 + i;
-    const uint4 ck = ldg_stream(k_cache + row * D + lane * 16);
-    const uint4 cv = ldg_stream(v_cache + row * D + lane * 16);
-    const float sk = k_scale[row], sv = v_scale[row];
-    const size_t dst = ((size_t)b * N + i) * D + lane * 16;
-    uint4 lo, hi;
-    dequant16(ck, sk, lo, hi);
-    reinterpret_cast<uint4*>(k + dst)[0] = lo;
-    reinterpret_cast<uint4*>(k + dst)[1] = hi;
-    dequant16(cv, sv, lo, hi);
-    reinterpret_cast<uint4*>(v + dst)[0] = lo;
-    reinterpret_cast<uint4*>(v + dst)[1] = hi;
+    const int i0 = blockIdx.x * (RPB * kRows) + threadIdx.x / LPR;
+    uint2 c[2 * kRows];
+    float s[2 * kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const int i = min(i0 + r * RPB, n - 1);  // (n = 0: nothing is stored, row s0 - 1 or 0 is read)
+        const size_t row = (size_t)b * Tmax + max(s0 + i, 0);
+        c[2 * r] = ldg_stream8(k_cache + row * D + lane * 8);
+        c[2 * r + 1] = ldg_stream8(v_cache + row * D + lane * 8);
+        s[2 * r] = __ldg(k_scale + row);
+        s[2 * r + 1] = __ldg(v_scale + row);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const int i = i0 + r * RPB;
+        if (i >= n) break;
+        const size_t dst = ((size_t)b * N + i) * D + lane * 8;
+        *reinterpret_cast<uint4*>(k + dst) = dequant8(c[2 * r], s[2 * r]);
+        *reinterpret_cast<uint4*>(v + dst) = dequant8(c[2 * r + 1], s[2 * r + 1]);
+    }
 }
 
 // ------------------------------------------------------------- paged cache
@@ -252,46 +289,57 @@ paged_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16*
     if (bad) atomicOr(flags, FLAG_NONFINITE);
 }
 
-// Rows [start, start + count) of each sequence, every KV head: a thread takes
-// one 16-code piece of K and of V.  grid (pieces / 256, B).
+constexpr int kPagedRows = 4;  // (a page number comes before each: 2 took 61 us where 4 take 57)
+
+// Rows [start, start + count) of each sequence and one KV head, as
+// token_read_kernel.  grid (rows, B, Hkv).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kThreads)
 paged_read_kernel(const uint8_t* __restrict__ k_pages, const uint8_t* __restrict__ v_pages,
                   const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                   const int32_t* __restrict__ table, const int32_t* __restrict__ start,
                   const int32_t* __restrict__ count, __nv_bfloat16* __restrict__ k,
-                  __nv_bfloat16* __restrict__ v, int N, int Hkv, int page, int n_pages,
-                  int max_pages, unsigned* __restrict__ flags) {
-    constexpr int LPR = D / 16;
-    const int b = blockIdx.y;
+                  __nv_bfloat16* __restrict__ v, int N, int log_page, int n_pages, int max_pages,
+                  unsigned* __restrict__ flags) {
+    constexpr int LPR = D / 8;
+    constexpr int RPB = kThreads / LPR;
+    const int b = blockIdx.y, h = blockIdx.z, Hkv = gridDim.z;
+    const int lane = threadIdx.x % LPR;
     const int s0 = start[b], n = count ? count[b] : N;
-    if (n < 0 || n > N || s0 < 0 || s0 > max_pages * page - n) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
+    if (n < 0 || n > N || s0 < 0 || s0 > (max_pages << log_page) - n) {
+        if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicOr(flags, FLAG_BAD_LENGTH);
         return;
     }
-    const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int lane = (int)(unit % LPR);
-    const int64_t row = unit / LPR;
-    const int i = (int)(row / Hkv), h = (int)(row % Hkv);
-    if (i >= n) return;
-    const int pos = s0 + i;
-    const int pid = table[(size_t)b * max_pages + pos / page];
-    if (pid < 0 || pid >= n_pages) {
-        atomicOr(flags, FLAG_BAD_INDEX);
-        return;
+    const int i0 = blockIdx.x * (RPB * kPagedRows) + threadIdx.x / LPR;
+    int pid[kPagedRows];
+    uint2 c[2 * kPagedRows];
+    float s[2 * kPagedRows];
+#pragma unroll
+    for (int r = 0; r < kPagedRows; r++) {
+        const int i = i0 + r * RPB;
+        pid[r] = i < n ? __ldg(table + (size_t)b * max_pages + ((s0 + i) >> log_page)) : 0;
     }
-    const size_t ph = (size_t)pid * Hkv + h;
-    const size_t at = (ph * page + pos % page) * D + lane * 16;
-    const uint4 ck = ldg_stream(k_pages + at), cv = ldg_stream(v_pages + at);
-    const float sk = k_scale[ph], sv = v_scale[ph];
-    const size_t dst = (((size_t)b * N + i) * Hkv + h) * D + lane * 16;
-    uint4 lo, hi;
-    dequant16(ck, sk, lo, hi);
-    reinterpret_cast<uint4*>(k + dst)[0] = lo;
-    reinterpret_cast<uint4*>(k + dst)[1] = hi;
-    dequant16(cv, sv, lo, hi);
-    reinterpret_cast<uint4*>(v + dst)[0] = lo;
-    reinterpret_cast<uint4*>(v + dst)[1] = hi;
+#pragma unroll
+    for (int r = 0; r < kPagedRows; r++) {
+        const int i = i0 + r * RPB;
+        const bool ok = i < n && pid[r] >= 0 && pid[r] < n_pages;
+        if (i < n && !ok) atomicOr(flags, FLAG_BAD_INDEX);
+        if (!ok) pid[r] = -1;
+        const size_t ph = (size_t)(ok ? pid[r] : 0) * Hkv + h;
+        const size_t at = ((ph << log_page) + (ok ? (s0 + i) & ((1 << log_page) - 1) : 0)) * D + lane * 8;
+        c[2 * r] = ldg_stream8(k_pages + at);
+        c[2 * r + 1] = ldg_stream8(v_pages + at);
+        s[2 * r] = __ldg(k_scale + ph);
+        s[2 * r + 1] = __ldg(v_scale + ph);
+    }
+#pragma unroll
+    for (int r = 0; r < kPagedRows; r++) {
+        const int i = i0 + r * RPB;
+        if (pid[r] < 0 || i >= n) continue;
+        const size_t dst = (((size_t)b * N + i) * Hkv + h) * D + lane * 8;
+        *reinterpret_cast<uint4*>(k + dst) = dequant8(c[2 * r], s[2 * r]);
+        *reinterpret_cast<uint4*>(v + dst) = dequant8(c[2 * r + 1], s[2 * r + 1]);
+    }
 }
 
 }  // namespace kvc
