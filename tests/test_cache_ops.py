@@ -258,7 +258,7 @@ def test_binding_refuses_host_strided_mistyped_and_misshaped_tensors(monkeypatch
         hs2._dense(rows, "v_new", (bf,), (2, 5, 128), 0)
     with pytest.raises(ValueError, match="v_new: must be a CUDA tensor"):
         hs2._dense(rows, "v_new", (bf,), rows.shape, 0)
-    assert hs2._dense(None, "count", (i32,), (2,), 0, True) is None
+    assert hs2._dense_or_none(None, "count", (i32,), (2,), 0) is None
     with pytest.raises(TypeError, match="count: expected a torch.Tensor"):
         hs2._dense(None, "count", (i32,), (2,), 0)
     del f32

@@ -21,6 +21,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -508,11 +509,15 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _INT_MAX = 2**31 - 1
 
 
-def _dense(t, name: str, dtypes, shape, dev: int, optional: bool = False):
+def _dense(t, name: str, dtypes, shape, dev: int):
     """Device pointer of a dense tensor of exactly this shape on device `dev`
     (the checks of _ptr, with the shape instead of the element count)."""
-    if t is None and optional:
-        return None
+    try:
+        if (t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+                and t.get_device() == dev):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -521,12 +526,16 @@ def _dense(t, name: str, dtypes, shape, dev: int, optional: bool = False):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous (dense, row-major)")
-    if t.get_device() != dev:
-        _check_device(name, t.device)
-    return t.data_ptr()
+    _check_device(name, t.device)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+
+
+def _dense_or_none(t, name: str, dtypes, shape, dev: int):
+    return None if t is None else _dense(t, name, dtypes, shape, dev)
 
 
 def _rank(t, name: str, rank: int):
+    """Shape of a CUDA tensor of this rank."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dim() != rank:
@@ -549,6 +558,21 @@ def paged_shape(B, Hkv, d, page, n_pages, max_pages) -> PagedShape:
     return PagedShape(B, Hkv, d, page, n_pages, max_pages)
 
 
+# the shapes of a program's calls, built once each
+_cache_shape = functools.lru_cache(maxsize=256)(CacheShape)
+_paged_shape = functools.lru_cache(maxsize=256)(PagedShape)
+_window_shape = functools.lru_cache(maxsize=256)(WindowShape)
+
+
+# the current stream's handle without building a Stream object (3 us of a call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+
+
 def hs2_kv_write(k_new, v_new, start, k_cache, v_cache, k_scale, v_scale, *, count=None,
                  stream=None) -> None:
     """Quantise K/V rows into the e4m3 token cache.  k_new, v_new [B,N,d] bf16;
@@ -558,12 +582,12 @@ def hs2_kv_write(k_new, v_new, start, k_cache, v_cache, k_scale, v_scale, *, cou
     dev = _current_device()
     rows, cache, scales = (B, N, d), (B, Tmax, d), (B, Tmax)
     st = load().hs2_kv_write(
-        CacheShape(B, Tmax, d), N, _dense(k_new, "k_new", _BF16, rows, dev),
+        _cache_shape(B, Tmax, d), N, _dense(k_new, "k_new", _BF16, rows, dev),
         _dense(v_new, "v_new", _BF16, rows, dev), _dense(start, "start", _I32, (B,), dev),
-        _dense(count, "count", _I32, (B,), dev, True),
+        _dense_or_none(count, "count", _I32, (B,), dev),
         _dense(k_cache, "k_cache", _E4M3, cache, dev), _dense(v_cache, "v_cache", _E4M3, cache, dev),
         _dense(k_scale, "k_scale", _F32, scales, dev), _dense(v_scale, "v_scale", _F32, scales, dev),
-        _stream(stream))
+        _raw_stream(stream, dev))
     _check(st, "hs2_kv_write")
 
 
@@ -576,11 +600,11 @@ def hs2_kv_read(k_cache, v_cache, k_scale, v_scale, start, N: int, *, count=None
     k = _alloc(stream, rows, torch.bfloat16, dev) if k is None else k
     v = _alloc(stream, rows, torch.bfloat16, dev) if v is None else v
     st = load().hs2_kv_read(
-        CacheShape(B, Tmax, d), N, _dense(k_cache, "k_cache", _E4M3, cache, dev),
+        _cache_shape(B, Tmax, d), N, _dense(k_cache, "k_cache", _E4M3, cache, dev),
         _dense(v_cache, "v_cache", _E4M3, cache, dev), _dense(k_scale, "k_scale", _F32, scales, dev),
         _dense(v_scale, "v_scale", _F32, scales, dev), _dense(start, "start", _I32, (B,), dev),
-        _dense(count, "count", _I32, (B,), dev, True), _dense(k, "k", _BF16, rows, dev),
-        _dense(v, "v", _BF16, rows, dev), _stream(stream))
+        _dense_or_none(count, "count", _I32, (B,), dev), _dense(k, "k", _BF16, rows, dev),
+        _dense(v, "v", _BF16, rows, dev), _raw_stream(stream, dev))
     _check(st, "hs2_kv_read")
     return k, v
 
@@ -589,7 +613,7 @@ def _paged(k_pages, v_pages, k_scale, v_scale, table, dev):
     """The shape of a paged cache and the pointers of its five tensors."""
     P, Hkv, page, d = pages = _rank(k_pages, "k_pages", 4)
     B, mp = _rank(table, "table", 2)
-    return PagedShape(B, Hkv, d, page, P, mp), (
+    return _paged_shape(B, Hkv, d, page, P, mp), (
         _dense(k_pages, "k_pages", _E4M3, pages, dev), _dense(v_pages, "v_pages", _E4M3, pages, dev),
         _dense(k_scale, "k_scale", _F32, (P, Hkv), dev),
         _dense(v_scale, "v_scale", _F32, (P, Hkv), dev), _dense(table, "table", _I32, (B, mp), dev))
@@ -607,8 +631,8 @@ def hs2_paged_kv_write(k_new, v_new, table, start, k_pages, v_pages, k_scale, v_
     rows = (B, N, shape.Hkv, shape.d)
     st = load().hs2_paged_kv_write(
         shape, N, _dense(k_new, "k_new", _BF16, rows, dev), _dense(v_new, "v_new", _BF16, rows, dev),
-        tb, _dense(start, "start", _I32, (B,), dev), _dense(count, "count", _I32, (B,), dev, True),
-        kp, vp, ks, vs, _stream(stream))
+        tb, _dense(start, "start", _I32, (B,), dev), _dense_or_none(count, "count", _I32, (B,), dev),
+        kp, vp, ks, vs, _raw_stream(stream, dev))
     _check(st, "hs2_paged_kv_write")
 
 
@@ -623,8 +647,8 @@ def hs2_paged_kv_read(k_pages, v_pages, k_scale, v_scale, table, start, N: int, 
     v = _alloc(stream, rows, torch.bfloat16, dev) if v is None else v
     st = load().hs2_paged_kv_read(
         shape, N, *ptrs, _dense(start, "start", _I32, (B,), dev),
-        _dense(count, "count", _I32, (B,), dev, True), _dense(k, "k", _BF16, rows, dev),
-        _dense(v, "v", _BF16, rows, dev), _stream(stream))
+        _dense_or_none(count, "count", _I32, (B,), dev), _dense(k, "k", _BF16, rows, dev),
+        _dense(v, "v", _BF16, rows, dev), _raw_stream(stream, dev))
     _check(st, "hs2_paged_kv_read")
     return k, v
 
@@ -653,9 +677,9 @@ def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, w
         shape, Hq, _INT_MAX if window is None else min(window, _INT_MAX), min(n_sink, _INT_MAX),
         1.0 / math.sqrt(d) if scale is None else scale, _dense(q, "q", _BF16, out, dev), *ptrs,
         _dense(lengths, "lengths", _I32, (shape.B,), dev), _dense(o, "o", _BF16, out, dev),
-        _dense(lse, "lse", _F32, out[:2], dev, True),
+        _dense_or_none(lse, "lse", _F32, out[:2], dev),
         _dense(workspace, "workspace", (workspace.dtype,), workspace.shape, dev),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     _check(st, "hs2_paged_decode")
     return o, lse
 
@@ -672,12 +696,12 @@ def hs2_window_attn(q, k, v, window: int, n_sink: int = 0, *, scale=None, o=None
     o = _alloc(stream, rows, torch.bfloat16, dev) if o is None else o
     if lse is None and want_lse:
         lse = _alloc(stream, rows[:3], torch.float32, dev)
-    shape = WindowShape(B, Lq, Lk, Hq, Hkv, d, min(window, _INT_MAX), min(n_sink, _INT_MAX),
+    shape = _window_shape(B, Lq, Lk, Hq, Hkv, d, min(window, _INT_MAX), min(n_sink, _INT_MAX),
                         1.0 / math.sqrt(d) if scale is None else scale)
     st = load().hs2_window_attn(
         shape, _dense(q, "q", _BF16, rows, dev), _dense(k, "k", _BF16, keys, dev),
         _dense(v, "v", _BF16, keys, dev), _dense(o, "o", _BF16, rows, dev),
-        _dense(lse, "lse", _F32, rows[:3], dev, True), _stream(stream))
+        _dense_or_none(lse, "lse", _F32, rows[:3], dev), _raw_stream(stream, dev))
     _check(st, "hs2_window_attn")
     return o, lse
 
