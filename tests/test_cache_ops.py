@@ -125,6 +125,7 @@ def paged(B=2, Hkv=2, d=128, page=64, n_pages=8, max_pages=4):
     (dict(B=65536), 1, hs2.HS2_ERR_INVALID_ARG),
     (dict(Tmax=0), 1, hs2.HS2_ERR_INVALID_ARG),
     (dict(d=96), 1, hs2.HS2_ERR_UNSUPPORTED),
+    (dict(Tmax=2**31 - 1), 1, hs2.HS2_ERR_UNSUPPORTED),
     (dict(), 0, hs2.HS2_ERR_INVALID_ARG),
     (dict(), 65, hs2.HS2_ERR_INVALID_ARG),
 ])
@@ -155,6 +156,7 @@ BAD_PAGED = [
     (dict(page=256), hs2.HS2_ERR_UNSUPPORTED),
     (dict(d=32), hs2.HS2_ERR_UNSUPPORTED),
     (dict(max_pages=2**25), hs2.HS2_ERR_UNSUPPORTED),
+    (dict(max_pages=2**25 - 1), hs2.HS2_ERR_UNSUPPORTED),     # positions up to 2^31 - 64
     (dict(n_pages=2**30, Hkv=2), hs2.HS2_ERR_UNSUPPORTED),
 ]
 
@@ -218,6 +220,8 @@ def test_paged_calls_reject_bad_arguments(lib):
     (dict(Hkv=0), hs2.HS2_ERR_INVALID_ARG),
     (dict(Hq=34), hs2.HS2_ERR_UNSUPPORTED),
     (dict(d=256), hs2.HS2_ERR_UNSUPPORTED),
+    (dict(Lk=2**31 - 1), hs2.HS2_ERR_UNSUPPORTED),
+    (dict(Lq=2**28, Lk=2**28, Hq=16, Hkv=1), hs2.HS2_ERR_UNSUPPORTED),  # 2^32 rows
 ])
 def test_window_rejects_bad_shapes(lib, fields, code):
     base = dict(B=1, Lq=16, Lk=64, Hq=4, Hkv=2, d=128, window=8, n_sink=0, scale=0.1)

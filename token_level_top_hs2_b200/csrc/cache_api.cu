@@ -16,6 +16,8 @@ using namespace hs2;
 namespace {
 
 constexpr int kMaxGroup = 16;  // query heads per KV head
+// Positions are 32-bit, and so are the ends of the tiles that hold them.
+constexpr int kMaxPositions = INT_MAX - 1024;
 constexpr int kMaxHeads = 4096;
 
 bool scale_ok(float s) { return s > 0.f && isfinite(s); }
@@ -41,7 +43,7 @@ bool pointers_ok(const P*... p) {
 hs2_status check_cache(const hs2_cache_shape* s) {
     if (!s) return HS2_ERR_INVALID_ARG;
     if (s->B < 1 || s->B > 65535 || s->Tmax < 1) return HS2_ERR_INVALID_ARG;
-    if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
+    if ((s->d != 64 && s->d != 128) || s->Tmax > kMaxPositions) return HS2_ERR_UNSUPPORTED;
     return HS2_OK;
 }
 
@@ -53,8 +55,8 @@ hs2_status check_paged(const hs2_paged_shape* s) {
     if (s->page != 16 && s->page != 32 && s->page != 64 && s->page != 128)
         return HS2_ERR_UNSUPPORTED;
     if (s->Hkv > kMaxHeads) return HS2_ERR_UNSUPPORTED;
-    // positions, and (page, head) numbers, are 32-bit
-    if ((int64_t)s->max_pages * s->page > INT_MAX) return HS2_ERR_UNSUPPORTED;
+    // (page, head) numbers are 32-bit too
+    if ((int64_t)s->max_pages * s->page > kMaxPositions) return HS2_ERR_UNSUPPORTED;
     if ((int64_t)s->n_pages * s->Hkv > INT_MAX) return HS2_ERR_UNSUPPORTED;
     return HS2_OK;
 }
@@ -331,16 +333,16 @@ hs2_status hs2_window_attn(const hs2_window_shape* shape, const void* q, const v
         return HS2_ERR_INVALID_ARG;
     hs2_status e = check_groups(s->Hq, s->Hkv);
     if (e != HS2_OK) return e;
-    if (s->d != 64 && s->d != 128) return HS2_ERR_UNSUPPORTED;
+    if ((s->d != 64 && s->d != 128) || s->Lk > kMaxPositions) return HS2_ERR_UNSUPPORTED;
     if (!pointers_ok(q, k, v, o) || !aligned16(lse)) return HS2_ERR_INVALID_ARG;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    unsigned* flags = device_flags();
-    if (!flags) return HS2_ERR_CUDA;
     const int G = s->Hq / s->Hkv, nt = win::BM / G;
     const int64_t blocks = ((int64_t)s->Lq + 2 * nt - 1) / (2 * nt);
     // items and rows are counted in 32 bits
     if (blocks * s->B * s->Hkv > INT_MAX || (int64_t)s->B * s->Lq * s->Hq > INT_MAX)
         return HS2_ERR_UNSUPPORTED;
+    unsigned* flags = device_flags();
+    if (!flags) return HS2_ERR_CUDA;
     const win::Shape sh = {s->B, s->Lq, s->Lk, s->Hq, s->Hkv, G, nt, s->window, s->n_sink, (int)blocks,
                            (int)(blocks * s->B * s->Hkv), s->scale * kLog2e};
     return s->d == 128 ? run_window<128>(sh, q, k, v, o, lse, st, flags)
