@@ -657,6 +657,12 @@ def hs2_paged_decode_workspace(shape: PagedShape, Hq: int) -> int:
     return load().hs2_paged_decode_workspace(ctypes.byref(shape), Hq)
 
 
+@functools.lru_cache(maxsize=256)
+def _paged_workspace(Hkv: int, d: int, Hq: int) -> int:
+    # (the workspace does not depend on the sequences, the page or the pool)
+    return hs2_paged_decode_workspace(PagedShape(1, Hkv, d, 64, 1, 1), Hq)
+
+
 def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, window=None,
                      n_sink: int = 0, scale=None, o=None, lse=None, workspace=None,
                      want_lse: bool = True, stream=None):
@@ -669,17 +675,18 @@ def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, w
     o = _alloc(stream, out, torch.bfloat16, dev) if o is None else o
     if lse is None and want_lse:
         lse = _alloc(stream, out[:2], torch.float32, dev)
-    lib = load()
     if workspace is None:
-        workspace = _alloc(stream, max(16, lib.hs2_paged_decode_workspace(shape, Hq)),
-                           torch.uint8, dev)
-    st = lib.hs2_paged_decode(
+        n_ws = _paged_workspace(shape.Hkv, shape.d, Hq)
+        workspace = _alloc(stream, max(16, n_ws), torch.uint8, dev)
+        ws = workspace.data_ptr()
+    else:
+        ws = _dense(workspace, "workspace", (workspace.dtype,), workspace.shape, dev)
+        n_ws = workspace.numel() * workspace.element_size()
+    st = load().hs2_paged_decode(
         shape, Hq, _INT_MAX if window is None else min(window, _INT_MAX), min(n_sink, _INT_MAX),
         1.0 / math.sqrt(d) if scale is None else scale, _dense(q, "q", _BF16, out, dev), *ptrs,
         _dense(lengths, "lengths", _I32, (shape.B,), dev), _dense(o, "o", _BF16, out, dev),
-        _dense_or_none(lse, "lse", _F32, out[:2], dev),
-        _dense(workspace, "workspace", (workspace.dtype,), workspace.shape, dev),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+        _dense_or_none(lse, "lse", _F32, out[:2], dev), ws, n_ws, _raw_stream(stream, dev))
     _check(st, "hs2_paged_decode")
     return o, lse
 
