@@ -145,13 +145,14 @@ hs2_status run_paged(const PagedCall& c) {
     const int64_t tiles = (seen / pgd::kTile + 3) * s->Hkv * s->B;
     const int grid = (int)std::min<int64_t>(tiles, sm_count());
     if (grid < 1) return HS2_ERR_CUDA;
+    auto* splits = reinterpret_cast<pgd::Split*>(c.part + (size_t)2 * pgd::kMaxCtas * (16 * D + 32));
     auto run = [&](auto kern, bool ok) {
         const size_t smem = pgd::Cfg<D, NG>::SMEM;
         if (!ok || !set_smem(kern, smem)) return HS2_ERR_CUDA;
         kern<<<grid, pgd::kThreads, smem, c.st>>>(
             mk, mv, static_cast<const __nv_bfloat16*>(c.q), c.ks, c.vs, c.table, work, c.G,
             s->n_pages, s->max_pages, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.lse,
-            c.part, c.flags);
+            c.part, splits, c.flags);
         return launch_status();
     };
     hs2_status e;
@@ -162,9 +163,9 @@ hs2_status run_paged(const PagedCall& c) {
         default: e = run(pgd::paged_decode_kernel<D, NG, 128>, registers_ok<D, NG, 128>());
     }
     if (e != HS2_OK) return e;
-    return launch_pdl(pgd::paged_merge_kernel<D>, dim3(s->Hkv * c.G, s->B), dim3(D), 0, c.st, work, c.G,
-                      grid, static_cast<__nv_bfloat16*>(c.o), c.lse,
-                      static_cast<const float*>(c.part)) == cudaSuccess
+    return launch_pdl(pgd::paged_merge_kernel<D>, dim3(grid, c.G), dim3(D), 0, c.st, c.G,
+                      static_cast<__nv_bfloat16*>(c.o), c.lse, static_cast<const float*>(c.part),
+                      static_cast<const pgd::Split*>(splits)) == cudaSuccess
                ? HS2_OK
                : HS2_ERR_CUDA;
 }
@@ -294,8 +295,8 @@ hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_
 
 size_t hs2_paged_decode_workspace(const hs2_paged_shape* shape, int Hq) {
     if (check_paged(shape) != HS2_OK || check_groups(Hq, shape->Hkv) != HS2_OK) return 0;
-    // two parts of an item per CTA
-    return (size_t)2 * pgd::kMaxCtas * (16 * shape->d + 32) * sizeof(float);
+    // two parts of an item per CTA, and what the merge is to do
+    return (size_t)pgd::kMaxCtas * (2 * (16 * shape->d + 32) * sizeof(float) + sizeof(pgd::Split));
 }
 
 hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, int n_sink,

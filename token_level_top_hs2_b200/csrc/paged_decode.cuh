@@ -67,6 +67,15 @@ HS2_DEV int length_of(const int32_t* lengths, int b, int cap, bool* bad) {
 // CTAs: CTA c of n takes [c * total / n, (c + 1) * total / n).
 HS2_DEV int64_t cut(int64_t total, int c, int n) { return (int64_t)c * total / n; }
 
+// The CTA that owns tile t of the line.
+HS2_DEV int owner(int64_t total, int64_t t, int n) { return (int)(((t + 1) * n + total - 1) / total) - 1; }
+
+// What a CTA leaves for the merge: where the parts of the item that it began
+// and did not end are.  parts 0: it began none.
+struct Split {
+    int row, first, parts, unused;  // (sequence, KV head), the item's first part, their number
+};
+
 struct Work {
     const int32_t* lengths;
     int B, cap, window, n_sink, Hkv;
@@ -233,7 +242,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     const int32_t* __restrict__ table, const Work work, int G, int n_pages,
                     int max_pages, float scale2, __nv_bfloat16* __restrict__ o,
                     float* __restrict__ lse, float* __restrict__ part,
-                    unsigned* __restrict__ flags) {
+                    Split* __restrict__ splits, unsigned* __restrict__ flags) {
     using C = Cfg<D, NG>;
     constexpr int NST = C::STAGES;
     constexpr uint32_t SWZ = D == 128 ? 2 : 4;         // 128- or 64-byte rows
@@ -275,6 +284,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         tma_prefetch_map(&map_k);
         tma_prefetch_map(&map_v);
     }
+    if (warp == 3 && lane == 0) splits[blockIdx.x] = Split{0, 0, 0, 0};
     if (warp == 2) {
         // the length of the whole line of tiles, and the item that the CTA starts in
         const int cta = blockIdx.x;
@@ -499,6 +509,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 mma_commit_w(&bars.drain[1]);
                 volatile int no_abort = 0;
                 mbar_wait(&bars.drain[1], 0, &no_abort, flags);
+            }
+        } else if (warp == 3) {
+            // ------------------------- sequences without visible tokens
+            const int row = Hkv * G * D;
+            for (int b = cta; b < work.B; b += gridDim.x) {
+                bool bad = false;
+                if (length_of(work.lengths, b, work.cap, &bad) > 0) continue;
+                for (int e = lane * 8; e < row; e += 256)
+                    *reinterpret_cast<uint4*>(o + (size_t)b * row + e) = make_uint4(0, 0, 0, 0);
+                if (lse)
+                    for (int h = lane; h < Hkv * G; h += 32) lse[(size_t)b * Hkv * G + h] = -INFINITY;
             }
         } else if (warp == 2) {
             // --------------------------------------------------- q's pieces
@@ -767,6 +788,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                                 lse[q0 + h] = any ? (R[h] + log2f(l[h])) * kLn2 : -INFINITY;
                         }
                     } else if (ok) {
+                        if (from_top && row == 0) {
+                            const int64_t end = cut(total, cta, n_cta) + i0 + w.s.tiles;
+                            splits[cta] = Split{w.b * Hkv + w.h, 2 * cta + (at_start ? 0 : 1),
+                                                owner(total, end - 1, n_cta) - cta + 1, 0};
+                        }
                         float* ps = part + (size_t)(2 * cta + (at_start ? 0 : 1)) * C::PART;
 #pragma unroll
                         for (int h = 0; h < NG; h++) {
@@ -795,45 +821,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
 }
 
-// Items cut between CTAs: their parts in the order of the line.  Sequences
-// without visible tokens get zeros.  grid (Hq, B), a thread per dim; the parts'
+// Items cut between CTAs: their parts in the order of the line.  grid (CTAs of
+// the kernel before, G): the item that CTA began, a thread per dim; the parts'
 // references and sums are read by a lane each, their outputs eight at a time.
 template <int D>
 __global__ void __launch_bounds__(D)
-paged_merge_kernel(const Work work, int G, int n_grid, __nv_bfloat16* __restrict__ o,
-                   float* __restrict__ lse, const float* __restrict__ part) {
+paged_merge_kernel(int G, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                   const float* __restrict__ part, const Split* __restrict__ splits) {
     constexpr int PART = 16 * D + 32;
-    __shared__ unsigned long long s_before, s_total;
     __shared__ float s_a[kMaxCtas];
-    const int tid = threadIdx.x, hk = blockIdx.x / G, h = blockIdx.x % G, b = blockIdx.y;
-    if (tid == 0) s_before = s_total = 0;
-    __syncthreads();
-    unsigned long long before = 0, total = 0;
-    bool bad = false;
-    for (int i = tid; i < work.B; i += D) {
-        const int nt = span_of(length_of(work.lengths, i, work.cap, &bad), work.window, work.n_sink).tiles;
-        total += nt;
-        if (i < b) before += nt;
-    }
-    if (total) atomicAdd(&s_total, total);
-    if (before) atomicAdd(&s_before, before);
-    __syncthreads();
-    const int64_t all = (int64_t)s_total * work.Hkv;
-    const int nt = span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
-    const size_t row = ((size_t)b * work.Hkv + hk) * G + h;
+    const int tid = threadIdx.x, c0 = blockIdx.x, h = blockIdx.y;
     griddep_wait();
-    if (nt == 0) {
-        o[row * D + tid] = __float2bfloat16(0.f);
-        if (lse && tid == 0) lse[row] = -INFINITY;
-        return;
-    }
-    const int n = (int)min((int64_t)n_grid, all);
-    const int64_t t0 = (int64_t)s_before * work.Hkv + (int64_t)hk * nt, t1 = t0 + nt;
-    auto owner = [&](int64_t t) { return (int)(((t + 1) * n + all - 1) / all) - 1; };
-    const int c0 = owner(t0), c1 = owner(t1 - 1), np = c1 - c0 + 1;
-    if (np == 1) return;
-    const int first = 2 * c0 + (cut(all, c0, n) == t0 ? 0 : 1);
-    auto at = [&](int i) { return part + (size_t)(i == 0 ? first : 2 * (c0 + i)) * PART; };
+    const Split sp = splits[c0];
+    const int np = sp.parts;
+    if (np == 0) return;
+    const size_t row = (size_t)sp.row * G + h;
+    auto at = [&](int i) { return part + (size_t)(i == 0 ? sp.first : 2 * (c0 + i)) * PART; };
     // every warp finds the common reference and the sum
     float M = -INFINITY, l = 0.f;
     for (int i = tid & 31; i < np; i += 32) M = fmaxf(M, at(i)[16 * D + h]);
