@@ -213,7 +213,7 @@ hs2_status hs2_kv_write(const hs2_cache_shape* shape, int N, const void* k_new, 
     unsigned* flags = device_flags();
     if (!flags) return HS2_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int rows = kvc::kThreads / (shape->d / 8) * kvc::kRows;
+    const int rows = kvc::kThreads / (shape->d / 16);
     const dim3 grid((N + rows - 1) / rows, shape->B);
     auto run = [&](auto kern) {
         kern<<<grid, kvc::kThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(k_new),

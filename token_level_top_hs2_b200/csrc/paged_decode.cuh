@@ -11,10 +11,13 @@
 //     each after a common power of two per KV head that puts max|q| in
 //     [128, 256).  Exact for every element above 2^-14 of the largest; below,
 //     the error is at most 2^-21 of the largest.
-//   * a weight w (nine significant bits, rounded to nearest) = three e5m2
-//     pieces of 3 bits each, the top bytes of an f16 and of its exact
-//     remainders.  e5m2 has no steps below 2^-16: smaller weights round to a
-//     multiple of it, with the largest weight kept between 2^11 and 2^15.
+//   * a weight w (nine significant bits, rounded to nearest) = a + b + c / 32,
+//     three e5m2 pieces of 3 bits each: the top bytes of an f16, of its exact
+//     remainder and of 32 times the next.  c's smallest step stands for 2^-21:
+//     smaller weights round to a multiple of it, with the largest weight
+//     kept between 2^8 and 2^14.  (Those six octaves are room for a maximum
+//     that grows: with c unscaled and three octaves, a batch with uneven pages
+//     raised its references 13 times per CTA and took 65.0 us, not 62.7.)
 // The pieces are columns of one MMA (N = 2 or 3 times the heads) and are summed
 // in fp32.  The page's K scale multiplies the logit, its V scale the weight.
 #pragma once
@@ -31,8 +34,8 @@ using kvc::e4m3x2;
 constexpr int kTile = 128;       // tokens per tile
 constexpr int kThreads = 512;    // QK, PV, q, -; four producers; two softmax groups of four
 constexpr int kMaxCtas = 148;    // one per SM
-constexpr float kTopLog2 = 11.f;    // a raised reference maps the largest weight to 2^11
-constexpr float kHalfStep = 7.62939453125e-6f;  // 2^-17, half of e5m2's smallest step
+constexpr float kTopLog2 = 8.f;     // a raised reference maps the largest weight to 2^8
+constexpr float kHalfStep = 2.384185791015625e-7f;  // 2^-22, half of the pieces' smallest step
 constexpr float kRaiseLog2 = 14.f;  // weights above 2^14 (before the V scale) raise it again
 
 // Scales of pages by their number in the CTA's line of tiles, modulo this: at
@@ -609,7 +612,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     }
                     float vnew = vref;
 #pragma unroll
-                    for (int u = 0; u < 4; u++) vnew = fmaxf(vnew, bars.red[g][u][16]);
+                    for (int u = 0; u < 4; u++) vnew = fmaxf(vnew, 2.f * bars.red[g][u][16]);
                     const float beta = vnew > 0.f ? vref / vnew : 0.f;
                     vref = vnew;
                     vinv = vnew > 0.f ? 1.f / vnew : 0.f;
@@ -650,7 +653,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     const float p0 = vis ? ex2(y[h]) : 0.f, p1 = vis ? ex2(y[h + 1]) : 0.f;
                     l[h] += p0;
                     l[h + 1] += p1;
-                    // nine significant bits, and no step below 2^-16: half a step of
+                    // nine significant bits, and no step below 2^-21: half a step of
                     // each added, what is below it cut
                     pc[h / 2] = (pack_f16(fmaf(p0, rv, kHalfStep), fmaf(p1, rv, kHalfStep)) + 0x00020002u) &
                                 0xFFFCFFFCu;
@@ -665,10 +668,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                                                   *reinterpret_cast<const __half2*>(&t));
                         return *reinterpret_cast<const uint32_t*>(&d);
                     };
+                    auto times32 = [](uint32_t x) {
+                        const __half2 d = __hmul2(*reinterpret_cast<__half2*>(&x), __float2half2_rn(32.f));
+                        return *reinterpret_cast<const uint32_t*>(&d);
+                    };
                     b1[j] = prmt(x0, x1, 0x7531u);
                     x0 = rest(x0), x1 = rest(x1);
                     b2[j] = prmt(x0, x1, 0x7531u);
-                    x0 = rest(x0), x1 = rest(x1);
+                    x0 = times32(rest(x0)), x1 = times32(rest(x1));
                     b3[j] = prmt(x0, x1, 0x7531u);
                 }
                 if (k > 0) ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
@@ -736,7 +743,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                         tmem_ld16(o_col + c, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[h]);
+                        for (int h = 0; h < NG; h++) O[h] = fmaf(__uint_as_float(v[h]), c == C::NP - 16 ? 0.03125f : 1.f, O[h]);
                     }
                 }
                 fence_before_sync();
