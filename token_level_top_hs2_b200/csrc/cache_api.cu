@@ -118,16 +118,18 @@ struct PagedCall {
     unsigned* flags;
 };
 
+template <class K>
+int launch_registers(K kernel) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
+}
+
 // The registers that the kernel's setmaxnreg splits are 512 x 128: it must have
 // been built to launch with exactly those (its warps would wait for them in vain).
 template <int D, int NG, int PAGE>
 bool registers_ok() {
     if (NG != 16) return true;
-    static const bool ok = [] {
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, pgd::paged_decode_kernel<D, NG, PAGE>) == cudaSuccess &&
-               a.numRegs == 128;
-    }();
+    static const bool ok = launch_registers(pgd::paged_decode_kernel<D, NG, PAGE>) == 128;
     return ok;
 }
 
@@ -191,7 +193,9 @@ hs2_status run_window(const win::Shape& s, const void* q, const void* k, const v
         return HS2_ERR_CUDA;
     const int grid = std::min(s.items, sm_count());
     const size_t smem = win::Cfg<D>::SMEM;
-    if (grid < 1 || !set_smem(win::window_attn_kernel<D>, smem)) return HS2_ERR_CUDA;
+    // (setmaxnreg in the kernel, as in registers_ok)
+    static const bool built = launch_registers(win::window_attn_kernel<D>) == 128;
+    if (!built || grid < 1 || !set_smem(win::window_attn_kernel<D>, smem)) return HS2_ERR_CUDA;
     win::window_attn_kernel<D><<<grid, win::kThreads, smem, st>>>(
         m, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse, s, flags);

@@ -18,8 +18,9 @@
 // is done: the chain softmax -> PV -> QK^T -> softmax of a single buffer is cut.
 //   warps 0, 2  TMA producers: queries (two items) and the K ring; the V ring
 //   warps 1, 3  MMA issuers of tiles 0 and 1: S_x = Q_x K^T, O_x += P_x V
-//   warps 4-7   softmax of tile 0, thread = row = TMEM lane
-//   warps 8-11  softmax of tile 1
+//   warps 4-7   outputs of both tiles: accumulator, maximum and sum to o and lse
+//   warps 8-11  softmax of tile 0, thread = row = TMEM lane
+//   warps 12-15 softmax of tile 1
 // P (bf16, as V is) overwrites its logits; the running maximum is raised only
 // when a tile exceeds it by 2^8, so the accumulator is rarely rescaled.
 #pragma once
@@ -33,7 +34,7 @@ using namespace hs2::tc;
 
 constexpr int BM = 128;           // rows of a tile
 constexpr int BN = 64;            // keys of a tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr float kRaiseLog2 = 8.f;
 
 struct Shape {
@@ -137,8 +138,8 @@ struct Cfg {
     static constexpr int KT = BN * D * 2;            // a K or V tile
     static constexpr int OFF_K = 4 * QT;             // (two items of two tiles before it)
     static constexpr int OFF_V = OFF_K + 2 * KT;
-    static constexpr int OFF_O = OFF_V + 2 * KT;     // 32 rows x 64 columns per softmax warp
-    static constexpr int SMEM = OFF_O + 8 * 4096 + 1024;
+    static constexpr int OFF_O = OFF_V + 2 * KT;     // 32 rows x 64 columns per output warp
+    static constexpr int SMEM = OFF_O + 4 * 4096 + 1024;
     static constexpr uint32_t COL_O = 256;           // S: [tile][buffer] of 64 columns
 };
 
@@ -150,6 +151,8 @@ struct Bars {
     // [rows' tile][tile & 1]: a softmax warp can be one ahead of the thread that
     // waits for it, so each barrier is used every other time
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
+    uint64_t ml_full[2][2], o_free[2];  // [rows' tile][item & 1]; [rows' tile]
+    float2 ml[2][2][BM];                // [rows' tile][item & 1]: a row's maximum and sum
     uint32_t tmem;
     int abort_;
 };
@@ -183,10 +186,12 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             mbar_init(&bars.k_full[i], 1);
             mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.drain[i], 1);
+            mbar_init(&bars.o_free[i], 4);
             for (int j = 0; j < 2; j++) {
                 mbar_init(&bars.s_full[i][j], 1);
                 mbar_init(&bars.p_full[i][j], 4);
                 mbar_init(&bars.pv_done[i][j], 1);
+                mbar_init(&bars.ml_full[i][j], 4);
             }
         }
         bars.abort_ = 0;
@@ -209,6 +214,10 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     Walk w;
     w.start(sh, blockIdx.x);
 
+    // Registers go where they are needed: the 65,536 that 512 threads launch
+    // with are 128 x (40 + 136 + 168 + 168).
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------- producers
         // Warp 0 loads queries and K, warp 2 V.  The queries of the next item
@@ -274,7 +283,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         const uint64_t v0 = sdesc_sw128(base + C::OFF_V, BN * 128, 1024);
         constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
         const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
-        int ca = 0, cw = 0;  // tiles whose logits and whose outputs are issued
+        int ca = 0, cw = 0, items = 0;  // tiles whose logits and whose outputs are issued; items of those
         // of a tile, until its PV: rows / 16, and 256 if it opens its item
         uint32_t next[2] = {0, 0};
         auto qk = [&]() {
@@ -308,13 +317,16 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         }
         while (ok && cw < ca) {
             const bool more = !w.done(sh);
+            // an item's first product overwrites the accumulator of the one before
+            const bool opens = next[0] >= 256;
+            if (opens && items++ > 0 && !wait_warp(&bars.o_free[x], items & 1, abort_, flags)) break;
             if (!wait_warp(&bars.v_full[cw & 1], (cw >> 1) & 1, abort_, flags) || (more && !ready()) ||
                 !wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags))
                 break;
             fence_after_sync();
             const uint64_t dv = v0 + (((cw & 1) * C::KT) >> 4);
             const uint32_t p = s_col + (cw & 1) * 64, n = next[0] & 255;
-            mma_ts_w(o_col, p, dv, id_pv, next[0] < 256);
+            mma_ts_w(o_col, p, dv, id_pv, !opens);
 #pragma unroll
             for (int ks = 1; ks < BN / 16; ks++)
                 if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
@@ -327,73 +339,92 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
         mma_commit_w(&bars.drain[x]);
         volatile int no_abort = 0;
         mbar_wait(&bars.drain[x], 0, &no_abort, flags);
+    }
+    } else if (warp < 8) {
+        // ------------------------------------------------------ outputs
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int tok = row / sh.G, head = row - tok * sh.G;
+        uint4* stage = reinterpret_cast<uint4*>(smem + C::OFF_O + (warp - 4) * 4096);
+        bool ok = true;
+        for (int c = 0; ok && !w.done(sh); w.n += step, w.count++) {
+            const Item it = item_of(sh, w.n);
+            c += it.tiles;
+            for (int x = 0; ok && x < 2; x++) {
+                ok = __all_sync(~0u, mbar_wait(&bars.ml_full[x][w.count & 1], (w.count >> 1) & 1, abort_,
+                                               flags) &&
+                                         mbar_wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
+                                                   abort_, flags));
+                if (!ok) break;
+                fence_after_sync();
+                const float2 ml = bars.ml[x][w.count & 1][row];
+                const int i = it.i0 + x * sh.nt + tok;
+                const bool real = tok < sh.nt && i < sh.Lq;
+                const float inv = 1.f / ml.y;
+                // NaN once anything is not finite
+                __nv_bfloat162 zero = __float2bfloat162_rn(ml.y * 0.f);
+                const __nv_bfloat162 nought = __float2bfloat162_rn(0.f);
+                uint32_t p[D / 2];
+#pragma unroll
+                for (int u = 0; u < D; u += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(lanes + C::COL_O + x * D + u, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int z = 0; z < 32; z += 2) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[z]) * inv,
+                                                                       __uint_as_float(r[z + 1]) * inv);
+                        zero = __hfma2(v, nought, zero);
+                        p[(u + z) / 2] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.o_free[x]);
+                const int at = real ? (it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head : -1;
+                // through the warp's shared memory, 64 columns at a time, so that
+                // each store instruction writes whole 128-byte lines of four rows
+#pragma unroll
+                for (int u = 0; u < D; u += 64) {
+#pragma unroll
+                    for (int z = 0; z < 8; z++) {
+                        const uint32_t* e = p + u / 2 + z * 4;
+                        stage[lane * 8 + (z ^ (lane & 7))] = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int z = 0; z < 8; z++) {
+                        const int r4 = z * 4 + (lane >> 3), to = __shfl_sync(~0u, at, r4);
+                        const uint4 v = stage[r4 * 8 + ((lane & 7) ^ (r4 & 7))];
+                        if (to >= 0)
+                            *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 7) * 8) = v;
+                    }
+                    __syncwarp();
+                }
+                if (lse && real) lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
+                const bool fine = __low2float(zero) + __high2float(zero) == 0.f;
+                unsigned spoilt = __ballot_sync(~0u, real && !fine);
+                const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
+                for (; spoilt; spoilt &= spoilt - 1) {
+                    const int src = __ffs(spoilt) - 1;
+                    const size_t a = __shfl_sync(~0u, at, src);
+                    attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
+                                  it.t0 + __shfl_sync(~0u, i, src) - it.i0, sh.window, sh.n_sink,
+                                  sh.scale2, o + a * D, lse ? lse + a : nullptr);
+                }
+            }
+        }
     } else {
         // ------------------------------------------------------ softmax
-        const int x = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        // (waits in line: a call would keep the compiler from the extra registers)
+        const int x = (warp >> 2) - 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + x * D;
-        const int tok = row / sh.G, head = row - tok * sh.G;
+        const int tok = row / sh.G;
         bool ok = true;
         int c = 0;
-        // The result of an item's tile is taken while the next item's first
-        // weights wait to be used: PV of its last tile is done by then.
-        uint4* stage = reinterpret_cast<uint4*>(smem + C::OFF_O + (warp - 4) * 4096);
-        auto finish = [&](const Item& it, float m, float l) {
-            ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1, abort_, flags));
-            if (!ok) return;
-            fence_after_sync();
-            const int i = it.i0 + x * sh.nt + tok;
-            const bool real = tok < sh.nt && i < sh.Lq;
-            const float inv = 1.f / l;
-            // NaN once anything is not finite
-            __nv_bfloat162 zero = __float2bfloat162_rn(l * 0.f);
-            const __nv_bfloat162 nought = __float2bfloat162_rn(0.f);
-            const int at = real ? (it.b * sh.Lq + i) * sh.Hq + it.hk * sh.G + head : -1;
-            // through the warp's shared memory, 64 columns at a time, so that
-            // each store instruction writes whole 128-byte lines of four rows
-#pragma unroll 1
-            for (int u = 0; u < D; u += 64) {
-                uint32_t r[2][32];
-                tmem_ld32(o_col + u, r[0]);
-                tmem_ld32(o_col + u + 32, r[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int z = 0; z < 8; z++) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const int e = 8 * (z & 3) + 2 * y;
-                        const __nv_bfloat162 v =
-                            __floats2bfloat162_rn(__uint_as_float(r[z >> 2][e]) * inv,
-                                                  __uint_as_float(r[z >> 2][e + 1]) * inv);
-                        zero = __hfma2(v, nought, zero);
-                        p[y] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    stage[lane * 8 + (z ^ (lane & 7))] = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int z = 0; z < 8; z++) {
-                    const int r4 = z * 4 + (lane >> 3), to = __shfl_sync(~0u, at, r4);
-                    const uint4 v = stage[r4 * 8 + ((lane & 7) ^ (r4 & 7))];
-                    if (to >= 0) *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 7) * 8) = v;
-                }
-                __syncwarp();
-            }
-            if (lse && real) lse[at] = (m + __log2f(l)) * kLn2;
-            const bool fine = __low2float(zero) + __high2float(zero) == 0.f;
-            unsigned spoilt = __ballot_sync(~0u, real && !fine);
-            const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
-            for (; spoilt; spoilt &= spoilt - 1) {
-                const int src = __ffs(spoilt) - 1;
-                const size_t a = __shfl_sync(~0u, at, src);
-                attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
-                              it.t0 + __shfl_sync(~0u, i, src) - it.i0, sh.window, sh.n_sink, sh.scale2,
-                              o + a * D, lse ? lse + a : nullptr);
-            }
-        };
-        Item was = w.it;
-        float m_was = 0.f, l_was = 1.f;
         while (ok && !w.done(sh)) {
             const Item it = w.it;
             const int t = it.t0 + x * sh.nt + tok;
@@ -411,7 +442,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 const int e0 = j * BN;
                 const bool second = e0 + 32 < it.entries;  // (else PV reads the first 32 keys at most)
                 const uint32_t s_col = lanes + x * 128 + (c & 1) * 64;
-                ok = __all_sync(~0u, wait(&bars.s_full[x][c & 1], (c >> 1) & 1, abort_, flags));
+                ok = __all_sync(~0u, mbar_wait(&bars.s_full[x][c & 1], (c >> 1) & 1, abort_, flags));
                 if (!ok) break;
                 fence_after_sync();
                 float s[BN], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -446,7 +477,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                     l *= alpha;
                     if (j > 0) {
                         // O holds the sum up to tile j - 1: once that is there, rescale it
-                        ok = __all_sync(~0u, wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
+                        ok = __all_sync(~0u, mbar_wait(&bars.pv_done[x][(c - 1) & 1], ((c - 1) >> 1) & 1,
                                                   abort_, flags));
                         if (!ok) break;
                         fence_after_sync();
@@ -478,19 +509,17 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
-                if (j == 0 && w.count > 0) {
-                    finish(was, m_was, l_was);
-                    if (!ok) break;
-                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[x][c & 1]);
             }
-            was = it, m_was = m, l_was = l;
+            if (!ok) break;
+            bars.ml[x][w.count & 1][row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ml_full[x][w.count & 1]);
             w.j = it.tiles - 1;
             w.next(sh, step);
         }
-        if (ok && w.count > 0) finish(was, m_was, l_was);
     }
     fence_before_sync();
     __syncthreads();
