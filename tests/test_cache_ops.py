@@ -195,7 +195,7 @@ def test_paged_calls_reject_bad_arguments(lib):
     assert decode(Hq=34) == hs2.HS2_ERR_UNSUPPORTED         # 17 per KV head
     assert decode(window=0) == hs2.HS2_ERR_INVALID_ARG
     assert decode(n_sink=-1) == hs2.HS2_ERR_INVALID_ARG
-    for scale in (0.0, -1.0, float("nan"), float("inf")):
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert decode(scale=scale) == hs2.HS2_ERR_INVALID_ARG
     assert decode(ws=need - 1) == hs2.HS2_ERR_WORKSPACE
     for i in range(10):
@@ -216,6 +216,7 @@ def test_paged_calls_reject_bad_arguments(lib):
     (dict(n_sink=-1), hs2.HS2_ERR_INVALID_ARG),
     (dict(scale=0.0), hs2.HS2_ERR_INVALID_ARG),
     (dict(scale=float("inf")), hs2.HS2_ERR_INVALID_ARG),
+    (dict(scale=3e38), hs2.HS2_ERR_INVALID_ARG),
     (dict(Hq=5), hs2.HS2_ERR_INVALID_ARG),
     (dict(Hkv=0), hs2.HS2_ERR_INVALID_ARG),
     (dict(Hq=34), hs2.HS2_ERR_UNSUPPORTED),

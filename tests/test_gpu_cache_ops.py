@@ -598,3 +598,86 @@ def test_a_prompt_in_chunks_then_decode_steps(cuda_lib, d, Hkv, G, page):
             r = pool.oracle(qn, [t + 1], window, n_sink, scale)
             check_attention(on, ln, r, q_top(qn, Hkv), d, window + n_sink, 2.0**-9, True)
     assert status(hs2) == 0
+
+
+def test_window_attn_of_a_batch_padded_with_nan(cuda_lib):
+    """Whole padding, keys, values and queries, of NaN: the padding's own rows
+    come out NaN and quickly, the others as if it were not there."""
+    hs2, L, G, d, window = cuda_lib, 6000, 4, 64, 5000
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(2, L, G, d, generator=g).to(BF).cuda()
+    k, v = (torch.randn(2, L, 1, d, generator=g).to(BF).cuda() for _ in "kv")
+    o, lse = hs2.hs2_window_attn(q, k, v, window, 2)
+    n = 2345
+    for x in (q, k, v):
+        x[1, n:] = math.nan
+    o2, lse2 = hs2.hs2_window_attn(q, k, v, window, 2)
+    assert status(hs2) == 0
+    assert torch.equal(o2[0], o[0]) and torch.equal(lse2[0], lse[0])
+    assert o2[1, n:].isnan().all() and lse2[1, n:].isnan().all()
+    np.testing.assert_allclose(f64(o2[1, :n]), f64(o[1, :n]), rtol=2.0**-7, atol=2.0**-8)
+    np.testing.assert_allclose(f64(lse2[1, :n]), f64(lse[1, :n]), atol=1e-4)
+
+
+def test_two_window_calls_at_once_and_one_replayed(cuda_lib):
+    """Calls on two streams, and a captured call replayed with other inputs."""
+    hs2, L, G, d = cuda_lib, 3000, 8, 128
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn(1, L, G, d, generator=g).to(BF).cuda()
+    k, v = (torch.randn(1, L, 1, d, generator=g).to(BF).cuda() for _ in "kv")
+    want = hs2.hs2_window_attn(q, k, v, 300, 4)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(q), torch.empty(1, L, G, device="cuda")) for _ in range(2)]
+    for _ in range(10):
+        for (o, lse), s in zip(outs, streams):
+            hs2.hs2_window_attn(q, k, v, 300, 4, o=o, lse=lse, stream=s)
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    o, lse = outs[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs2.hs2_window_attn(q, k, v, 300, 4, o=o, lse=lse)
+    q.mul_(0.5)
+    graph.replay()
+    want = hs2.hs2_window_attn(q, k, v, 300, 4)
+    torch.cuda.synchronize()
+    assert status(hs2) == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("B,lengths", [(1, [0]), (3, [0, 0, 0]), (200, None)])
+def test_paged_decode_of_empty_and_many_sequences(cuda_lib, B, lengths):
+    """No tokens at all, and more sequences than a warp scans at once, most
+    items smaller than a CTA's share."""
+    hs2, d, Hkv, G, page = cuda_lib, 64, 2, 3, 16
+    if lengths is None:
+        lengths = [(37 * i) % 300 if i % 3 else 0 for i in range(B)]
+    pool = Pool(B, Hkv, d, page, max(1, -(-max(lengths) // page)), seed=B).fill(lengths, seed=B)
+    q = torch.randn(B, G * Hkv, d, generator=torch.Generator().manual_seed(B)).to(BF).cuda()
+    o, lse = torch.full_like(q, 7.0), torch.full((B, G * Hkv), 7.0, device="cuda")
+    hs2.hs2_paged_decode(q, *pool.args(), ints(lengths), o=o, lse=lse)
+    assert status(hs2) == 0
+    r = pool.oracle(q, lengths, 2**31 - 1, 0, 1 / math.sqrt(d))
+    check_attention(o, lse, r, q_top(q, Hkv), d, 300, 2.0**-9, True)
+
+
+def test_calls_on_a_side_stream_keep_their_memory(cuda_lib):
+    """What a call allocates for another stream is not reused under it."""
+    hs2, L, G, d = cuda_lib, 2000, 16, 128
+    g = torch.Generator().manual_seed(9)
+    q = torch.randn(1, L, G, d, generator=g).to(BF).cuda()
+    k, v = (torch.randn(1, L, 1, d, generator=g).to(BF).cuda() for _ in "kv")
+    pool = Pool(4, 1, d, 64, 40, seed=9).fill([2500] * 4, seed=9)
+    qd = torch.randn(4, G, d, generator=g).to(BF).cuda()
+    want, dec = hs2.hs2_window_attn(q, k, v, 400, 0)[0], hs2.hs2_paged_decode(qd, *pool.args(), ints([2500] * 4))[0]
+    lengths = ints([2500] * 4)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        o = hs2.hs2_window_attn(q, k, v, 400, 0, stream=s)[0]
+        od = hs2.hs2_paged_decode(qd, *pool.args(), lengths, stream=s)[0]
+        junk = [torch.full((1 << 20,), 9.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        del junk
+        assert torch.equal(o, want) and torch.equal(od, dec)

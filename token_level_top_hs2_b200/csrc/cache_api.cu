@@ -20,7 +20,8 @@ constexpr int kMaxGroup = 16;  // query heads per KV head
 constexpr int kMaxPositions = INT_MAX - 1024;
 constexpr int kMaxHeads = 4096;
 
-bool scale_ok(float s) { return s > 0.f && isfinite(s); }
+// (the kernels work with scale * log2 e)
+bool scale_ok(float s) { return s > 0.f && isfinite(s) && isfinite(s * kLog2e); }
 
 // SMs of the current device, at most one CTA of the persistent kernels each.
 int sm_count() {

@@ -43,17 +43,19 @@ struct Shape {
 };
 
 // One query row and head by one warp, in fp32: the running maximum and sum of
-// the softmax over the visible keys alone, one key at a time, so that nothing
-// a masked row holds is ever read.  Rows whose tensor-core result is not
-// finite come here: 0 * NaN is NaN there, so that a masked key row of NaN or
-// infinities (the padding of a padded batch) spoils the rows that share its
-// tile.  Lane i owns the D/32 dims from i * D/32.
+// the softmax over the visible keys alone, so that nothing a masked row holds
+// is ever read.  Rows whose tensor-core result is not finite come here:
+// 0 * NaN is NaN there, so that a masked key row of NaN or infinities (the
+// padding of a padded batch) spoils the rows that share its tile.  Lane i owns
+// the D/32 dims from i * D/32; the newest key first: a row of padding itself
+// meets its NaN at once, and ends there.
 template <int D>
 static __device__ __noinline__ void attend_row(const __nv_bfloat16* __restrict__ q,
-                                        const __nv_bfloat16* __restrict__ k,
-                                        const __nv_bfloat16* __restrict__ v, int64_t ld, int t,
-                                        int window, int n_sink, float scale2,
-                                        __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+                                               const __nv_bfloat16* __restrict__ k,
+                                               const __nv_bfloat16* __restrict__ v, int64_t ld,
+                                               int t, int window, int n_sink, float scale2,
+                                               __nv_bfloat16* __restrict__ o,
+                                               float* __restrict__ lse) {
     constexpr int E = D / 32;
     const int lane = lane_id();
     float qf[E], acc[E], m = -INFINITY, l = 0.f;
@@ -64,7 +66,8 @@ static __device__ __noinline__ void attend_row(const __nv_bfloat16* __restrict__
     }
     const int w0 = max(0, t - window + 1);  // (t - window does not wrap: both are >= 0)
     const int ns = min(n_sink, w0);
-    for (int i = 0; i < ns + t + 1 - w0; i++) {
+    for (int i = ns + t - w0; i >= 0; i--) {
+        if (__any_sync(~0u, l != l)) break;  // (the lanes agree; a vote keeps their registers few)
         const int s = i < ns ? i : w0 + i - ns;
         float x = 0.f;
 #pragma unroll
@@ -217,129 +220,129 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
     // Registers go where they are needed: the 65,536 that 512 threads launch
     // with are 128 x (40 + 136 + 168 + 168).
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0 || warp == 2) {
-        // ------------------------------------------------- producers
-        // Warp 0 loads queries and K, warp 2 V.  The queries of the next item
-        // go out ahead of this item's last tile.
-        const bool is_v = warp == 2;
-        const CUtensorMap* m64 = is_v ? &maps.v64 : &maps.k64;
-        const CUtensorMap* m16 = is_v ? &maps.v16 : &maps.k16;
-        uint64_t* full = is_v ? bars.v_full : bars.k_full;
-        uint64_t(*taken)[2] = is_v ? bars.pv_done : bars.s_full;
-        const uint32_t ring = base + (is_v ? C::OFF_V : C::OFF_K);
-        int c = 0, q_armed = 0;  // tiles and items loaded
-        bool ok = true;
-        auto load_q = [&](const Item& it, int count) {
-            const int set = count & 1;
-            ok = wait_warp(&bars.q_empty[set], ((count >> 1) & 1) ^ 1, abort_, flags);
-            if (!ok) return;
-            mbar_arrive_expect_tx_w(&bars.q_full[set], 2 * C::DB * 128 * sh.G * sh.nt);
-            for (int x = 0; x < 2; x++)
-                for (int db = 0; db < C::DB; db++)
-                    tma_load_4d_w(base + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
-                                  it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
-            q_armed++;
-        };
-        if (!is_v && !w.done(sh)) load_q(w.it, 0);
-        while (ok && !w.done(sh)) {
-            const int rows = rows_of(w.it, w.j), e0 = w.j * BN;
-            const int st = c & 1;
-            // (the first two pass)
-            if (!wait_warp(&taken[0][st], ((c >> 1) & 1) ^ 1, abort_, flags) ||
-                !wait_warp(&taken[1][st], ((c >> 1) & 1) ^ 1, abort_, flags))
-                break;
-            mbar_arrive_expect_tx_w(&full[st], rows * D * 2);
-            const uint32_t dst = ring + st * C::KT;
-            if (rows == BN && e0 >= w.it.pre) {
-                for (int db = 0; db < C::DB; db++)
-                    tma_load_4d_w(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
-                                  w.it.base + e0 - w.it.pre, w.it.b, &full[st]);
-            } else {
-                for (int r = 0; r < rows; r += 16) {
-                    const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0 || warp == 2) {
+            // ------------------------------------------------- producers
+            // Warp 0 loads queries and K, warp 2 V.  The queries of the next item
+            // go out ahead of this item's last tile.
+            const bool is_v = warp == 2;
+            const CUtensorMap* m64 = is_v ? &maps.v64 : &maps.k64;
+            const CUtensorMap* m16 = is_v ? &maps.v16 : &maps.k16;
+            uint64_t* full = is_v ? bars.v_full : bars.k_full;
+            uint64_t(*taken)[2] = is_v ? bars.pv_done : bars.s_full;
+            const uint32_t ring = base + (is_v ? C::OFF_V : C::OFF_K);
+            int c = 0, q_armed = 0;  // tiles and items loaded
+            bool ok = true;
+            auto load_q = [&](const Item& it, int count) {
+                const int set = count & 1;
+                ok = wait_warp(&bars.q_empty[set], ((count >> 1) & 1) ^ 1, abort_, flags);
+                if (!ok) return;
+                mbar_arrive_expect_tx_w(&bars.q_full[set], 2 * C::DB * 128 * sh.G * sh.nt);
+                for (int x = 0; x < 2; x++)
                     for (int db = 0; db < C::DB; db++)
-                        tma_load_4d_w(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
-                                      w.it.b, &full[st]);
+                        tma_load_4d_w(base + (2 * set + x) * C::QT + db * (BM * 128), &maps.q, 64 * db,
+                                      it.hk * sh.G, it.i0 + x * sh.nt, it.b, &bars.q_full[set]);
+                q_armed++;
+            };
+            if (!is_v && !w.done(sh)) load_q(w.it, 0);
+            while (ok && !w.done(sh)) {
+                const int rows = rows_of(w.it, w.j), e0 = w.j * BN;
+                const int st = c & 1;
+                // (the first two pass)
+                if (!wait_warp(&taken[0][st], ((c >> 1) & 1) ^ 1, abort_, flags) ||
+                    !wait_warp(&taken[1][st], ((c >> 1) & 1) ^ 1, abort_, flags))
+                    break;
+                mbar_arrive_expect_tx_w(&full[st], rows * D * 2);
+                const uint32_t dst = ring + st * C::KT;
+                if (rows == BN && e0 >= w.it.pre) {
+                    for (int db = 0; db < C::DB; db++)
+                        tma_load_4d_w(dst + db * (BN * 128), m64, 64 * db, w.it.hk,
+                                      w.it.base + e0 - w.it.pre, w.it.b, &full[st]);
+                } else {
+                    for (int r = 0; r < rows; r += 16) {
+                        const int e = e0 + r, pos = e < w.it.pre ? e : w.it.base + e - w.it.pre;
+                        for (int db = 0; db < C::DB; db++)
+                            tma_load_4d_w(dst + db * (BN * 128) + r * 128, m16, 64 * db, w.it.hk, pos,
+                                          w.it.b, &full[st]);
+                    }
                 }
+                c++;
+                if (!is_v && w.j == w.it.tiles - 1 && w.n + step < sh.items)
+                    load_q(item_of(sh, w.n + step), w.count + 1);
+                w.next(sh, step);
             }
-            c++;
-            if (!is_v && w.j == w.it.tiles - 1 && w.n + step < sh.items)
-                load_q(item_of(sh, w.n + step), w.count + 1);
-            w.next(sh, step);
-        }
-        if (*abort_) {  // let the copies in flight land before the CTA leaves
+            if (*abort_) {  // let the copies in flight land before the CTA leaves
+                volatile int no_abort = 0;
+                for (int i = max(0, q_armed - 2); i < q_armed; i++)
+                    mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
+                for (int i = max(0, c - 2); i < c; i++)
+                    mbar_wait(&full[i & 1], (i >> 1) & 1, &no_abort, flags);
+            }
+        } else if (warp == 1 || warp == 3) {
+            // ----------------------------------------------- MMA issuers
+            const int x = warp >> 1;
+            const uint64_t q0 = sdesc_sw128(base + x * C::QT, 16, 1024);
+            const uint64_t k0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
+            const uint64_t v0 = sdesc_sw128(base + C::OFF_V, BN * 128, 1024);
+            constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
+            const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
+            int ca = 0, cw = 0, items = 0;  // tiles whose logits and whose outputs are issued; items of those
+            // of a tile, until its PV: rows / 16, and 256 if it opens its item
+            uint32_t next[2] = {0, 0};
+            auto qk = [&]() {
+                const uint32_t rows = rows_of(w.it, w.j);
+                const uint32_t id = idesc_bf16_f32(BM, 0, false, false) | (rows >> 3 << 17);
+                const uint64_t dq = q0 + ((2 * (w.count & 1) * C::QT) >> 4);
+                const uint64_t dk = k0 + (((ca & 1) * C::KT) >> 4);
+                const uint32_t d = s_col + (ca & 1) * 64;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++)
+                    mma_ss_w(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
+                             dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
+                mma_commit_w(&bars.s_full[x][ca & 1]);
+                if (w.j == w.it.tiles - 1) mma_commit_w(&bars.q_empty[w.count & 1]);
+                const uint32_t info = rows >> 4 | (w.j == 0 ? 256u : 0u);
+                ca++;
+                w.next(sh, step);
+                return info;
+            };
+            auto ready = [&]() {  // the next tile's operands
+                return (w.j > 0 || wait_warp(&bars.q_full[w.count & 1], (w.count >> 1) & 1, abort_, flags)) &&
+                       wait_warp(&bars.k_full[ca & 1], (ca >> 1) & 1, abort_, flags);
+            };
+            bool ok = true;
+            for (int i = 0; i < 2; i++) {
+                if (w.done(sh)) break;
+                ok = ok && ready();
+                if (!ok) break;
+                fence_after_sync();
+                next[i] = qk();
+            }
+            while (ok && cw < ca) {
+                const bool more = !w.done(sh);
+                // an item's first product overwrites the accumulator of the one before
+                const bool opens = next[0] >= 256;
+                if (opens && items++ > 0 && !wait_warp(&bars.o_free[x], items & 1, abort_, flags)) break;
+                if (!wait_warp(&bars.v_full[cw & 1], (cw >> 1) & 1, abort_, flags) || (more && !ready()) ||
+                    !wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags))
+                    break;
+                fence_after_sync();
+                const uint64_t dv = v0 + (((cw & 1) * C::KT) >> 4);
+                const uint32_t p = s_col + (cw & 1) * 64, n = next[0] & 255;
+                mma_ts_w(o_col, p, dv, id_pv, !opens);
+#pragma unroll
+                for (int ks = 1; ks < BN / 16; ks++)
+                    if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
+                mma_commit_w(&bars.pv_done[x][cw & 1]);
+                next[0] = next[1];
+                if (more) next[1] = qk();
+                cw++;
+            }
+            // every MMA issued must finish before TMEM is released
+            mma_commit_w(&bars.drain[x]);
             volatile int no_abort = 0;
-            for (int i = max(0, q_armed - 2); i < q_armed; i++)
-                mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, &no_abort, flags);
-            for (int i = max(0, c - 2); i < c; i++)
-                mbar_wait(&full[i & 1], (i >> 1) & 1, &no_abort, flags);
+            mbar_wait(&bars.drain[x], 0, &no_abort, flags);
         }
-    } else if (warp == 1 || warp == 3) {
-        // ----------------------------------------------- MMA issuers
-        const int x = warp >> 1;
-        const uint64_t q0 = sdesc_sw128(base + x * C::QT, 16, 1024);
-        const uint64_t k0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
-        const uint64_t v0 = sdesc_sw128(base + C::OFF_V, BN * 128, 1024);
-        constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
-        const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
-        int ca = 0, cw = 0, items = 0;  // tiles whose logits and whose outputs are issued; items of those
-        // of a tile, until its PV: rows / 16, and 256 if it opens its item
-        uint32_t next[2] = {0, 0};
-        auto qk = [&]() {
-            const uint32_t rows = rows_of(w.it, w.j);
-            const uint32_t id = idesc_bf16_f32(BM, 0, false, false) | (rows >> 3 << 17);
-            const uint64_t dq = q0 + ((2 * (w.count & 1) * C::QT) >> 4);
-            const uint64_t dk = k0 + (((ca & 1) * C::KT) >> 4);
-            const uint32_t d = s_col + (ca & 1) * 64;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ks++)
-                mma_ss_w(d, dq + (((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
-                         dk + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), id, ks > 0);
-            mma_commit_w(&bars.s_full[x][ca & 1]);
-            if (w.j == w.it.tiles - 1) mma_commit_w(&bars.q_empty[w.count & 1]);
-            const uint32_t info = rows >> 4 | (w.j == 0 ? 256u : 0u);
-            ca++;
-            w.next(sh, step);
-            return info;
-        };
-        auto ready = [&]() {  // the next tile's operands
-            return (w.j > 0 || wait_warp(&bars.q_full[w.count & 1], (w.count >> 1) & 1, abort_, flags)) &&
-                   wait_warp(&bars.k_full[ca & 1], (ca >> 1) & 1, abort_, flags);
-        };
-        bool ok = true;
-        for (int i = 0; i < 2; i++) {
-            if (w.done(sh)) break;
-            ok = ok && ready();
-            if (!ok) break;
-            fence_after_sync();
-            next[i] = qk();
-        }
-        while (ok && cw < ca) {
-            const bool more = !w.done(sh);
-            // an item's first product overwrites the accumulator of the one before
-            const bool opens = next[0] >= 256;
-            if (opens && items++ > 0 && !wait_warp(&bars.o_free[x], items & 1, abort_, flags)) break;
-            if (!wait_warp(&bars.v_full[cw & 1], (cw >> 1) & 1, abort_, flags) || (more && !ready()) ||
-                !wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags))
-                break;
-            fence_after_sync();
-            const uint64_t dv = v0 + (((cw & 1) * C::KT) >> 4);
-            const uint32_t p = s_col + (cw & 1) * 64, n = next[0] & 255;
-            mma_ts_w(o_col, p, dv, id_pv, !opens);
-#pragma unroll
-            for (int ks = 1; ks < BN / 16; ks++)
-                if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
-            mma_commit_w(&bars.pv_done[x][cw & 1]);
-            next[0] = next[1];
-            if (more) next[1] = qk();
-            cw++;
-        }
-        // every MMA issued must finish before TMEM is released
-        mma_commit_w(&bars.drain[x]);
-        volatile int no_abort = 0;
-        mbar_wait(&bars.drain[x], 0, &no_abort, flags);
-    }
     } else if (warp < 8) {
         // ------------------------------------------------------ outputs
         asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
