@@ -304,7 +304,8 @@ hs2_status hs2_decode_sparse_staged(const hs2_decode_shape* shape, const void* q
  * Rows that a call writes or reads: `start` [B] int32 (device) gives each
  * sequence's first cache position, `count` [B] int32 (device, may be NULL: N
  * each) how many of the N rows of k_new / v_new / k / v it uses, from row 0;
- * zero is allowed.  Rows past the count are neither read nor written.  A
+ * zero is allowed; N is at most a sequence's capacity (Tmax, or max_pages *
+ * page).  Rows past the count are not written and reach nothing.  A
  * sequence whose start or count is out of range (count outside [0, N], start
  * outside [0, capacity - count]) is left alone, as is a page number outside
  * [0, n_pages); both raise HS2_ERR_DEVICE_DATA as above.
@@ -375,7 +376,8 @@ hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_
  * last `window` of them or among the first `n_sink` (window = INT_MAX: all).
  *   Hq       query heads, a multiple of Hkv, at most 16 per KV head; query
  *            head h reads KV head h / (Hq / Hkv)
- *   q        [B, Hq, d] bf16, finite
+ *   q        [B, Hq, d] bf16, finite: infinities and NaN are flagged, and the
+ *            outputs of their KV head's query heads mean nothing
  *   k_pages, v_pages, k_scale, v_scale: any scales that are finite and > 0
  *   lengths  [B] int32, device, each in [0, max_pages * page]; a length of 0
  *            gives o = 0 and lse = -inf, one out of range the same and a flag

@@ -198,6 +198,9 @@ def test_paged_calls_reject_bad_arguments(lib):
     for scale in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert decode(scale=scale) == hs2.HS2_ERR_INVALID_ARG
     assert decode(ws=need - 1) == hs2.HS2_ERR_WORKSPACE
+    crowd = hs2.PagedShape(65535, 64, 64, 128, 1, 8192)  # 2^35 tiles of 128 tokens and more
+    assert lib.hs2_paged_decode(crowd, 64, 2**31 - 1, 0, 0.1, *PTR[:10], 1 << 30, None) \
+        == hs2.HS2_ERR_UNSUPPORTED
     for i in range(10):
         a = list(PTR[:10])
         a[i] = FAKE + 4

@@ -680,11 +680,12 @@ def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, w
         workspace = _alloc(stream, max(16, n_ws), torch.uint8, dev)
         ws = workspace.data_ptr()
     else:
-        ws = _dense(workspace, "workspace", (workspace.dtype,), workspace.shape, dev)
+        ws = _dense(workspace, "workspace", (getattr(workspace, "dtype", None),),
+                    getattr(workspace, "shape", None), dev)
         n_ws = workspace.numel() * workspace.element_size()
     st = load().hs2_paged_decode(
         shape, Hq, _INT_MAX if window is None else min(window, _INT_MAX), min(n_sink, _INT_MAX),
-        1.0 / math.sqrt(d) if scale is None else scale, _dense(q, "q", _BF16, out, dev), *ptrs,
+        1.0 / math.sqrt(d) if scale is None else float(scale), _dense(q, "q", _BF16, out, dev), *ptrs,
         _dense(lengths, "lengths", _I32, (shape.B,), dev), _dense(o, "o", _BF16, out, dev),
         _dense_or_none(lse, "lse", _F32, out[:2], dev), ws, n_ws, _raw_stream(stream, dev))
     _check(st, "hs2_paged_decode")
@@ -704,7 +705,7 @@ def hs2_window_attn(q, k, v, window: int, n_sink: int = 0, *, scale=None, o=None
     if lse is None and want_lse:
         lse = _alloc(stream, rows[:3], torch.float32, dev)
     shape = _window_shape(B, Lq, Lk, Hq, Hkv, d, min(window, _INT_MAX), min(n_sink, _INT_MAX),
-                        1.0 / math.sqrt(d) if scale is None else scale)
+                          1.0 / math.sqrt(d) if scale is None else float(scale))
     st = load().hs2_window_attn(
         shape, _dense(q, "q", _BF16, rows, dev), _dense(k, "k", _BF16, keys, dev),
         _dense(v, "v", _BF16, keys, dev), _dense(o, "o", _BF16, rows, dev),

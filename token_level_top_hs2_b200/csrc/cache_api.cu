@@ -134,6 +134,12 @@ bool registers_ok() {
     return ok;
 }
 
+// The most tiles that a call's sequences and heads can have together.
+int64_t paged_tiles(const hs2_paged_shape* s, int window, int n_sink) {
+    const int64_t seen = std::min<int64_t>(s->max_pages * s->page, (int64_t)window + n_sink);
+    return (seen / pgd::kTile + 3) * s->Hkv * s->B;
+}
+
 template <int D, int NG>
 hs2_status run_paged(const PagedCall& c) {
     const hs2_paged_shape* s = c.s;
@@ -144,9 +150,7 @@ hs2_status run_paged(const PagedCall& c) {
     const int cap = s->max_pages * s->page;
     const pgd::Work work = {c.lengths, s->B, cap, c.window, c.n_sink, s->Hkv};
     // no more CTAs than tiles there can be
-    const int64_t seen = std::min<int64_t>(cap, (int64_t)c.window + c.n_sink);
-    const int64_t tiles = (seen / pgd::kTile + 3) * s->Hkv * s->B;
-    const int grid = (int)std::min<int64_t>(tiles, sm_count());
+    const int grid = (int)std::min<int64_t>(paged_tiles(s, c.window, c.n_sink), sm_count());
     if (grid < 1) return HS2_ERR_CUDA;
     auto* splits = reinterpret_cast<pgd::Split*>(c.part + (size_t)2 * pgd::kMaxCtas * (16 * D + 32));
     auto run = [&](auto kern, bool ok) {
@@ -314,6 +318,8 @@ hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, in
     e = check_groups(Hq, shape->Hkv);
     if (e != HS2_OK) return e;
     if (window < 1 || n_sink < 0 || !scale_ok(scale)) return HS2_ERR_INVALID_ARG;
+    // a CTA counts its tiles in 32 bits
+    if (paged_tiles(shape, window, n_sink) > INT_MAX) return HS2_ERR_UNSUPPORTED;
     if (!pointers_ok(q, k_pages, v_pages, k_scale, v_scale, table, lengths, o) || !aligned16(lse) ||
         !pointers_ok(workspace))
         return HS2_ERR_INVALID_ARG;

@@ -222,10 +222,11 @@ paged_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16*
         if (blockIdx.x == 0 && tid == 0) atomicOr(flags, FLAG_BAD_LENGTH);
         return;
     }
-    const int slot = s0 / PAGE + (int)(blockIdx.x >> 1) / Hkv;
-    const int p0 = max(0, s0 - slot * PAGE), p1 = min(PAGE, s0 + n - slot * PAGE);
+    // rows [first, first + PAGE) of the call, counted from its first page's start
+    const int nth = (int)(blockIdx.x >> 1) / Hkv, lead = s0 % PAGE, first = nth * PAGE - lead;
+    const int p0 = nth == 0 ? lead : 0, p1 = min(PAGE, n - first);
     if (p0 >= p1) return;  // the rows do not reach this page
-    const int pid = table[(size_t)b * max_pages + slot];
+    const int pid = table[(size_t)b * max_pages + (s0 / PAGE + nth)];
     if (pid < 0 || pid >= n_pages) {
         if (tid == 0) atomicOr(flags, FLAG_BAD_INDEX);
         return;
@@ -239,7 +240,7 @@ paged_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16*
     for (int u = 0; u < U; u++) {
         const int unit = u * kPageThreads + tid, r = unit / LPR;
         const bool in = r >= p0 && r < p1;
-        const size_t i = (size_t)b * N + (slot * PAGE + r - s0);
+        const size_t i = (size_t)b * N + (first + r);
         w[u] = in ? ldg_stream(src + (i * Hkv + h) * D + (unit % LPR) * 8) : make_uint4(0, 0, 0, 0);
     }
     const float had = p0 > 0 ? *scale : 0.f;

@@ -108,7 +108,7 @@ HS2_DEV Item item_of(const Shape& s, int n) {
     const bool joined = s.n_sink > w0 - 16;
     it.base = joined && s.n_sink > 0 ? 0 : w0;
     it.pre = joined || s.n_sink == 0 ? 0 : (s.n_sink + 15) & ~15;
-    it.entries = it.pre + last + 1 - it.base;
+    it.entries = it.pre - it.base + last + 1;
     it.tiles = (it.entries + BN - 1) / BN;
     return it;
 }
@@ -433,13 +433,13 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             const int t = it.t0 + x * sh.nt + tok;
             // the row's keys as entries: [0, e_sink) and [e_lo, e_hi)
             const int e_sink = min(sh.n_sink, t + 1);
-            const int e_lo = it.pre + max(t - sh.window + 1, 0) - it.base;
-            const int e_hi = it.pre + t + 1 - it.base;
+            const int e_lo = it.pre - it.base + max(t - sh.window + 1, 0);
+            const int e_hi = it.pre - it.base + t + 1;
             // entries that every row of the tile sees: from the last row's window
             // start up to the first row
             const int t_min = it.t0 + x * sh.nt;
-            const int all_lo = it.pre + max(t_min + sh.nt - sh.window, 0) - it.base;
-            const int all_hi = it.pre + t_min + 1 - it.base;
+            const int all_lo = it.pre - it.base + max(t_min + sh.nt - sh.window, 0);
+            const int all_hi = it.pre - it.base + t_min + 1;
             float m = -1e30f, l = 0.f;
             for (int j = 0; j < it.tiles; j++, c++) {
                 const int e0 = j * BN;
