@@ -18,8 +18,8 @@
 //     kept between 2^8 and 2^14.  (Those six octaves are room for a maximum
 //     that grows: with c unscaled and three octaves, a batch with uneven pages
 //     raised its references 13 times per CTA and took 65.0 us, not 62.7.)
-// The pieces are columns of one MMA (N = 2 or 3 times the heads) and are summed
-// in fp32.  The page's K scale multiplies the logit, its V scale the weight.
+// The pieces are columns of one MMA (N = 2 or 3 times the heads, rounded up to
+// 16) and are summed in fp32.  The page's K scale multiplies the logit, its V scale the weight.
 #pragma once
 
 #include "kv_cache.cuh"
@@ -112,8 +112,8 @@ template <int D, int NG>
 struct Cfg {
     static constexpr int KV = kTile * D;             // bytes of a K or V tile
     static constexpr int STAGES = D == 128 ? 6 : 12;
-    static constexpr int NQ = 2 * NG;                // columns of a logit tile
-    static constexpr int PLANES = NG == 16 ? 3 : 2;  // 16-byte planes of weight pieces per token
+    static constexpr int NQ = NG == 4 ? 16 : 2 * NG;  // columns of a logit tile (4 heads leave half unread)
+    static constexpr int PLANES = (3 * NG + 15) / 16;  // 16-byte planes of weight pieces per token
     static constexpr int NP = 16 * PLANES;           // columns of an output accumulator
     static constexpr int PB = PLANES * kTile * 16;   // bytes of a weight tile
     static constexpr int QB = NQ * D;                // bytes of an item's q pieces
@@ -185,8 +185,10 @@ template <int N>
 HS2_DEV void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
     if constexpr (N == 32)
         tmem_ld32(taddr, r);
-    else
+    else if constexpr (N == 16)
         tmem_ld16(taddr, r);
+    else
+        tmem_ld8(taddr, r);
 }
 
 // One warp splits the G <= NG queries of an item (rows of D bf16) into the
@@ -579,8 +581,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 ok = ok && mbar_wait(&bars.s_full[sb], (k >> 1) & 1, abort_, flags);
                 fence_after_sync();
                 const float f = vis ? sc.x * bars.sqf[sb] : 0.f;
-                uint32_t r[C::NQ];
-                tmem_ldn<C::NQ>(lanes + sb * 32, r);
+                uint32_t r[2 * NG];
+                tmem_ldn<2 * NG>(lanes + sb * 32, r);
                 tmem_ld_wait();
                 fence_before_sync();
                 __syncwarp();
@@ -684,9 +686,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
                     *reinterpret_cast<uint4*>(p + kTile * 16) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
                     *reinterpret_cast<uint4*>(p + kTile * 32) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
-                } else {
+                } else if constexpr (NG == 8) {
                     *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b2[0], b2[1]);
                     *reinterpret_cast<uint4*>(p + kTile * 16) = make_uint4(b3[0], b3[1], 0u, 0u);
+                } else {
+                    *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b2[0], b3[0], 0u);
                 }
                 if (!vis) {
                     // 0 * NaN is NaN: a row that is not visible must not hold one
@@ -737,6 +741,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     if constexpr (NG == 8) {
 #pragma unroll
                         for (int h = 0; h < NG; h++) O[h] += __uint_as_float(v[8 + h]);
+                    }
+                    if constexpr (NG == 4) {
+#pragma unroll
+                        for (int h = 0; h < NG; h++)
+                            O[h] = fmaf(__uint_as_float(v[8 + h]), 0.03125f, O[h] + __uint_as_float(v[4 + h]));
                     }
 #pragma unroll
                     for (int c = 16; c < C::NP; c += 16) {
