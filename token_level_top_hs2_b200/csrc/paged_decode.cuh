@@ -19,7 +19,13 @@
 //     that grows: with c unscaled and three octaves, a batch with uneven pages
 //     raised its references 13 times per CTA and took 65.0 us, not 62.7.)
 // The pieces are columns of one MMA (N = 2 or 3 times the heads, rounded up to
-// 16) and are summed in fp32.  The page's K scale multiplies the logit, its V scale the weight.
+// 16) and are summed in fp32.  The page's K scale multiplies the logit, its V
+// scale the weight.
+//
+// Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 180 us or
+// 5.97 TB/s, 92% of a copy's rate; 48 ragged sequences with a window of 4096,
+// 8 KV heads of 64 and groups of four (202 MB), 55.4 us or 3.65 TB/s, bound by
+// the softmax warps' latency per tile; one sequence of 1k tokens 12.4 us.
 #pragma once
 
 #include "kv_cache.cuh"
@@ -348,10 +354,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         if constexpr (NG == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp >= 4) {
             // ------------------------------------------------------ producers
-            // Warps 4 and 6 load K, 5 and 7 V, of every other tile: a warp's
-            // copies move at most 14 bytes per cycle whatever their size (its
-            // scheduler's share of the copy engine), two warps' 24 to 28, four
-            // warps' what the memory gives, 30 to 33.
+            // Warps 4 and 6 load K, 5 and 7 V, of every other tile (D = 64; D =
+            // 128: 4 and 5 of all tiles): a warp's copies move at most 14 bytes
+            // per cycle whatever their size (its scheduler's share of the copy
+            // engine), two warps' 24 to 28, four warps' what the memory gives, 30
+            // to 33.  At D = 128 four warps took 183 us against two warps' 179,
+            // since SMs then get unequal shares of the memory; at D = 64, with
+            // half the bytes per tile, 67.7 against 74.
             // A lane per page: 32 pages (a batch of TPB of the warp's tiles) at a
             // time, whose numbers and scales are fetched while the tiles before
             // them are issued.

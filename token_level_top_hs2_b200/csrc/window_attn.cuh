@@ -23,6 +23,12 @@
 //   warps 12-15 softmax of tile 1
 // P (bf16, as V is) overwrites its logits; the running maximum is raised only
 // when a tile exceeds it by 2^8, so the accumulator is rarely rescaled.
+//
+// Measured: 128k queries of 16 heads of 128, window 128 (1.15 GB), 246 us or
+// 4.67 TB/s, bound by the chain of an item's softmax steps (most of its tiles
+// of keys are partly masked); 2 x 16k queries of 32 heads in 8 groups, window
+// 4096 (2.16 TF), 2.0 ms or 1.07 PF/s at the power cap, 55% of the tensor
+// pipe's cycles, bound by exponentials and power.
 #pragma once
 
 #include "tc.cuh"
