@@ -72,12 +72,18 @@ HS2_DEV int length_of(const int32_t* lengths, int b, int cap, bool* bad) {
     return 0;
 }
 
-// The tiles of all (sequence, KV head) items in one line, cut evenly over the
-// CTAs: CTA c of n takes [c * total / n, (c + 1) * total / n).
-HS2_DEV int64_t cut(int64_t total, int c, int n) { return (int64_t)c * total / n; }
-
-// The CTA that owns tile t of the line.
-HS2_DEV int owner(int64_t total, int64_t t, int n) { return (int)(((t + 1) * n + total - 1) / total) - 1; }
+// The tiles of all (sequence, KV head) items in one line (at most 2^31 - 1, as
+// the host checks), cut evenly over the CTAs: each takes `each`, the first
+// `more` of them one more.
+struct Cut {
+    int each, more;
+    HS2_DEV int start(int cta) const { return cta * each + min(cta, more); }
+    // the CTA that owns tile t
+    HS2_DEV int owner(int t) const {
+        const int big = more * (each + 1);
+        return t < big ? t / (each + 1) : more + (t - big) / each;
+    }
+};
 
 // What a CTA leaves for the merge: where the parts of the item that it began
 // and did not end are.  parts 0: it began none.
@@ -143,8 +149,8 @@ struct Bars {
     float sqf[4];           // the same per logit buffer
     float red[2][4][20];    // per group and warp: per-head maxima or sums, largest V scale
     float xr[16], xl[16];
-    int64_t total;
-    int b0, h0, t0;
+    Cut cut;
+    int n_cta, b0, h0, t0;  // CTAs with tiles; where this one starts
     uint32_t tmem;
     int abort_;
 };
@@ -300,35 +306,34 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         // the length of the whole line of tiles, and the item that the CTA starts in
         const int cta = blockIdx.x;
         bool bad = false;
-        int64_t sum = 0;
+        int total = 0;
 #pragma unroll 4
         for (int b = lane; b < work.B; b += 32)
-            sum += span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
+            total += span_of(length_of(work.lengths, b, work.cap, &bad), work.window, work.n_sink).tiles;
         if (bad && cta == 0) atomicOr(flags, FLAG_BAD_LENGTH);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(~0u, sum, off);
-        const int64_t total = sum * Hkv;
-        const int n = (int)min((int64_t)gridDim.x, total);
-        if (lane == 0) bars.total = total, bars.b0 = bars.h0 = bars.t0 = 0;
+        total = __reduce_add_sync(~0u, total) * Hkv;
+        const int n = min((int)gridDim.x, total);
+        const Cut cut = {n > 0 ? total / n : 0, n > 0 ? total % n : 0};
+        if (lane == 0) bars.cut = cut, bars.n_cta = n, bars.b0 = bars.h0 = bars.t0 = 0;
         __syncwarp();
         if (cta < n) {
-            const int64_t first = cut(total, cta, n);
-            int64_t before = 0;
+            const int first = cut.start(cta);
+            int before = 0;
             for (int b = 0; b < work.B && before * Hkv <= first; b += 32) {
                 const int nt = b + lane < work.B ? span_of(length_of(work.lengths, b + lane, work.cap, &bad),
                                                            work.window, work.n_sink).tiles
                                                  : 0;
-                int64_t upto = nt;
+                int upto = nt;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
-                    const int64_t u = __shfl_up_sync(~0u, upto, off);
+                    const int u = __shfl_up_sync(~0u, upto, off);
                     if (lane >= off) upto += u;
                 }
-                const int64_t at = first - (before + upto - nt) * Hkv;
-                if (at >= 0 && at < (int64_t)nt * Hkv) {
+                const int at = first - (before + upto - nt) * Hkv;
+                if (at >= 0 && at < nt * Hkv) {
                     bars.b0 = b + lane;
-                    bars.h0 = (int)(at / nt);
-                    bars.t0 = (int)(at % nt);
+                    bars.h0 = at / nt;
+                    bars.t0 = at % nt;
                 }
                 before += __shfl_sync(~0u, upto, 31);
             }
@@ -337,9 +342,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const int64_t total = bars.total;
-    const int n_cta = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-    const int n_tiles = cta < n_cta ? (int)(cut(total, cta + 1, n_cta) - cut(total, cta, n_cta)) : 0;
+    const int cta = blockIdx.x;
+    const int n_tiles = cta < bars.n_cta ? bars.cut.each + (cta < bars.cut.more ? 1 : 0) : 0;
     const uint32_t tmem = __shfl_sync(~0u, bars.tmem, 0);
     const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
     Walk w = {};
@@ -808,15 +812,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                             if (h >= G) break;
                             const bool any = l[h] != 0.f;
                             if (row < D)
-                                o[(q0 + h) * D + row] = __float2bfloat16(any ? O[h] / l[h] : 0.f);
+                                o[(q0 + h) * D + row] = __float2bfloat16(any ? O[h] * __frcp_rn(l[h]) : 0.f);
                             if (lse && row == h)
                                 lse[q0 + h] = any ? (R[h] + log2f(l[h])) * kLn2 : -INFINITY;
                         }
                     } else if (ok) {
                         if (from_top && row == 0) {
-                            const int64_t end = cut(total, cta, n_cta) + i0 + w.s.tiles;
+                            const int last = bars.cut.start(cta) + i0 + w.s.tiles - 1;
                             splits[cta] = Split{w.b * Hkv + w.h, 2 * cta + (at_start ? 0 : 1),
-                                                owner(total, end - 1, n_cta) - cta + 1, 0};
+                                                bars.cut.owner(last) - cta + 1, 0};
                         }
                         float* ps = part + (size_t)(2 * cta + (at_start ? 0 : 1)) * C::PART;
 #pragma unroll
