@@ -331,7 +331,7 @@ hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, in
                          o,     lse, static_cast<float*>(workspace), Hq / shape->Hkv, window, n_sink,
                          scale, st, flags};
     // a thread's exponentials and registers go by the heads it is built for: 48
-    // ragged sequences of 8 KV heads of 64 with groups of four take 55.4 us built
+    // ragged sequences of 8 KV heads of 64 with groups of four took 55.4 us built
     // for four heads, 63.3 for eight and 86.1 for sixteen
     if (shape->d == 128)
         return c.G > 8 ? run_paged<128, 16>(c) : c.G > 4 ? run_paged<128, 8>(c) : run_paged<128, 4>(c);

@@ -22,10 +22,13 @@
 // 16) and are summed in fp32.  The page's K scale multiplies the logit, its V
 // scale the weight.
 //
-// Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 180 us or
-// 5.97 TB/s, 92% of a copy's rate; 48 ragged sequences with a window of 4096,
-// 8 KV heads of 64 and groups of four (202 MB), 55.4 us or 3.65 TB/s, bound by
-// the softmax warps' latency per tile; one sequence of 1k tokens 12.4 us.
+// Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 179 us or
+// 6.0 TB/s, 93% of a copy's rate; 48 ragged sequences with a window of 4096,
+// 8 KV heads of 64 and groups of four (202 MB), 53.5 us or 3.8 TB/s, bound by
+// the softmax warps' latency per tile; one sequence of 1k tokens 12.4 us, of
+// which 7 are one tile's way through the kernel (13k cycles: 3,500 to the first
+// copy, 3,500 to its logits, 2,200 for a first reference, 1,400 for weights and
+// outputs, 2,500 for the part's end) and the merge most of the rest.
 #pragma once
 
 #include "kv_cache.cuh"
