@@ -157,10 +157,12 @@ struct Bars {
     // [tile & 1]: K and V have two places; that of tile c is free for tile c + 2
     // once both rows' tiles have taken theirs (s_full, pv_done)
     uint64_t k_full[2], v_full[2];
-    // [rows' tile][tile & 1]: a softmax warp can be one ahead of the thread that
-    // waits for it, so each barrier is used every other time
+    // [rows' tile][tile & 1]: a softmax warp can be one tile ahead of the thread
+    // that waits for it, so each barrier is used every other time
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
-    uint64_t ml_full[2][2], o_free[2];  // [rows' tile][item & 1]; [rows' tile]
+    // [rows' tile][item & 1]; [rows' tile].  o_free: the outputs have read an
+    // item's accumulator, and its maxima and sums before that
+    uint64_t ml_full[2][2], o_free[2];
     float2 ml[2][2][BM];                // [rows' tile][item & 1]: a row's maximum and sum
     uint32_t tmem;
     int abort_;
@@ -293,6 +295,12 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             constexpr uint32_t id_pv = idesc_bf16_f32(BM, D, false, true);
             const uint32_t s_col = tmem + x * 128, o_col = tmem + C::COL_O + x * D;
             int ca = 0, cw = 0, items = 0;  // tiles whose logits and whose outputs are issued; items of those
+            int freed = 0;                  // items whose accumulator the outputs have read
+            auto o_free = [&](int n) {      // the first n items'
+                while (freed < n)
+                    if (!wait_warp(&bars.o_free[x], freed++ & 1, abort_, flags)) return false;
+                return true;
+            };
             // of a tile, until its PV: rows / 16, and 256 if it opens its item
             uint32_t next[2] = {0, 0};
             auto qk = [&]() {
@@ -328,7 +336,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 const bool more = !w.done(sh);
                 // an item's first product overwrites the accumulator of the one before
                 const bool opens = next[0] >= 256;
-                if (opens && items++ > 0 && !wait_warp(&bars.o_free[x], items & 1, abort_, flags)) break;
+                if (opens && !o_free(items++)) break;
                 if (!wait_warp(&bars.v_full[cw & 1], (cw >> 1) & 1, abort_, flags) || (more && !ready()) ||
                     !wait_warp(&bars.p_full[x][cw & 1], (cw >> 1) & 1, abort_, flags))
                     break;
@@ -341,7 +349,13 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                     if (ks < n) mma_ts_w(o_col, p + ks * 8, dv + ((ks * 2048) >> 4), id_pv, 1u);
                 mma_commit_w(&bars.pv_done[x][cw & 1]);
                 next[0] = next[1];
-                if (more) next[1] = qk();
+                if (more) {
+                    // (an item's maxima and sums go where those of two items before
+                    // were, which the outputs must have read: items of one tile in a
+                    // row are ordered by nothing else)
+                    if (w.j == w.it.tiles - 1 && !o_free(w.count - 1)) break;
+                    next[1] = qk();
+                }
                 cw++;
             }
             // every MMA issued must finish before TMEM is released
