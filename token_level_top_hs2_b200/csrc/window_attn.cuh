@@ -82,6 +82,7 @@ static __device__ __noinline__ void attend_row(const __nv_bfloat16* __restrict__
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
         const float mn = fmaxf(m, x);
+        if (x == -INFINITY && m == x) continue;  // (no weight yet: -inf less -inf would be NaN)
         const float a = ex2(m - mn), p = ex2(x - mn);
         m = mn;
         l = fmaf(l, a, p);
