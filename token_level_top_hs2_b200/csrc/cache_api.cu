@@ -202,8 +202,9 @@ hs2_status run_window(const win::Shape& s, const void* q, const void* k, const v
     static const bool built = launch_registers(win::window_attn_kernel<D>) == 128;
     if (!built || grid < 1 || !set_smem(win::window_attn_kernel<D>, smem)) return HS2_ERR_CUDA;
     win::window_attn_kernel<D><<<grid, win::kThreads, smem, st>>>(
-        m, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-        static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse, s, flags);
+        m, {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(o), lse},
+        s, flags);
     return launch_status();
 }
 

@@ -18,7 +18,8 @@
 // is done: the chain softmax -> PV -> QK^T -> softmax of a single buffer is cut.
 //   warps 0, 2  TMA producers: queries (two items) and the K ring; the V ring
 //   warps 1, 3  MMA issuers of tiles 0 and 1: S_x = Q_x K^T, O_x += P_x V
-//   warps 4-7   outputs of both tiles: accumulator, maximum and sum to o and lse
+//   warps 4-7   outputs of both tiles: accumulator, maximum and sum to o and lse;
+//               at the end, rows that masked NaN or infinities have spoilt
 //   warps 8-11  softmax of tile 0, thread = row = TMEM lane
 //   warps 12-15 softmax of tile 1
 // P (bf16, as V is) overwrites its logits; the running maximum is raised only
@@ -30,6 +31,9 @@
 // 4096 (2.16 TF), 2.0 ms or 1.07 PF/s at the power cap, 55% of the tensor
 // pipe's cycles, bound by exponentials and power.
 #pragma once
+
+#include <float.h>
+#include <limits.h>
 
 #include "tc.cuh"
 
@@ -47,54 +51,11 @@ struct Shape {
     int B, Lq, Lk, Hq, Hkv, G, nt, window, n_sink, blocks, items;
     float scale2;
 };
-
-// One query row and head by one warp, in fp32: the running maximum and sum of
-// the softmax over the visible keys alone, so that nothing a masked row holds
-// is ever read.  Rows whose tensor-core result is not finite come here:
-// 0 * NaN is NaN there, so that a masked key row of NaN or infinities (the
-// padding of a padded batch) spoils the rows that share its tile.  Lane i owns
-// the D/32 dims from i * D/32; the newest key first: a row of padding itself
-// meets its NaN at once, and ends there.
-template <int D>
-static __device__ __noinline__ void attend_row(const __nv_bfloat16* __restrict__ q,
-                                               const __nv_bfloat16* __restrict__ k,
-                                               const __nv_bfloat16* __restrict__ v, int64_t ld,
-                                               int t, int window, int n_sink, float scale2,
-                                               __nv_bfloat16* __restrict__ o,
-                                               float* __restrict__ lse) {
-    constexpr int E = D / 32;
-    const int lane = lane_id();
-    float qf[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e++) {
-        qf[e] = __bfloat162float(q[lane * E + e]) * scale2;
-        acc[e] = 0.f;
-    }
-    const int w0 = max(0, t - window + 1);  // (t - window does not wrap: both are >= 0)
-    const int ns = min(n_sink, w0);
-    for (int i = ns + t - w0; i >= 0; i--) {
-        if (__any_sync(~0u, l != l)) break;  // (the lanes agree; a vote keeps their registers few)
-        const int s = i < ns ? i : w0 + i - ns;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e++)
-            x = fmaf(qf[e], __bfloat162float(k[s * ld + lane * E + e]), x);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
-        const float mn = fmaxf(m, x);
-        if (x == -INFINITY && m == x) continue;  // (no weight yet: -inf less -inf would be NaN)
-        const float a = ex2(m - mn), p = ex2(x - mn);
-        m = mn;
-        l = fmaf(l, a, p);
-#pragma unroll
-        for (int e = 0; e < E; e++)
-            acc[e] = fmaf(acc[e], a, p * __bfloat162float(v[s * ld + lane * E + e]));
-    }
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; e++) o[lane * E + e] = __float2bfloat16(acc[e] * inv);
-    if (lse && lane == 0) *lse = (m + log2f(l)) * kLn2;
-}
+struct Rows {
+    const __nv_bfloat16 *q, *k, *v;
+    __nv_bfloat16* o;
+    float* lse;
+};
 
 // The keys of an item as a list of entries: [0, pre) are positions 0 .. pre-1
 // (the sinks, rounded up to 16), entry e >= pre is position base + e - pre.
@@ -167,6 +128,7 @@ struct Bars {
     float2 ml[2][2][BM];                // [rows' tile][item & 1]: a row's maximum and sum
     uint32_t tmem;
     int abort_;
+    int redo_first, redo_last;          // the CTA's items with rows to do again
 };
 
 struct Maps {
@@ -177,12 +139,202 @@ struct Maps {
 // The low n bits (n <= 0: none, n >= 32: all).
 HS2_DEV uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 
+// Values of two bf16 in w that are not finite, as bits 0 and 1.
+HS2_DEV uint32_t not_finite(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 1u : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 2u : 0u);
+}
+
+// Barrier of the four warps of the outputs; true if any of their threads passes true.
+HS2_DEV bool outputs_any(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred)
+        : "memory");
+    return r != 0;
+}
+
+// An output row whose softmax itself is not finite (NaN, and so meant to be)
+// opens with this pair of NaN, whose sign no conversion to bf16 gives.
+constexpr uint32_t kMeantNan = 0xFFFFFFFFu;
+
+// Output dims that a key row out of the query's sight has spoilt, done again in
+// fp32 from the keys in sight.  0 * NaN is NaN on the tensor cores, so a masked
+// value row of NaN or infinities (the padding of a padded batch) spoils the
+// rows that share its tile; maxima and sums are never spoilt, since masked
+// logits are replaced.  The warps of the outputs come here once all of the CTA's
+// items are stored and no role waits for another, so it may take its time: a
+// row costs its window.  What keeps that rare: dims in which a key that the whole
+// item sees holds something not finite are right as they are (one pass over the
+// item's values finds them), a row is done from its newest key on and ends when
+// all of its dims have met such a value, and masked rows in a tile lie within
+// 2 nt + 15 positions of its queries or of their windows' starts.  Four rows and
+// 32 keys take about 5 us (a warp's own instructions: deeper batches of loads
+// change nothing): two sequences of 20,000 tokens, 4 heads of 128, plain causal,
+// 0.96 ms, with NaN from 11,111 on in the second 17.5 ms (398 ms with a row at a
+// time, a key per step, inside the pipeline).
+template <int D>
+static __device__ __noinline__ void redo_items(const Rows& io, const Shape& sh, int first, int last) {
+    extern __shared__ uint8_t smem_raw[];
+    float* shared = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~(uintptr_t)15);
+    constexpr int E = D / 32, W = E / 2;  // dims of a lane, in words
+    constexpr int R = 4;
+    const int lane = lane_id(), warp = threadIdx.x >> 5 & 3;
+    uint32_t* legit = reinterpret_cast<uint32_t*>(shared);  // [lane]: its dims not finite in common keys
+    float* qf = shared + 32 + warp * (R * D + 128);
+    float4* pw = reinterpret_cast<float4*>(qf + R * D);  // the rows' weights of 32 keys
+    // the lane's dims of a row, and which of them are not finite
+    auto dims = [&](const __nv_bfloat16* row, uint32_t (&w)[W]) {
+        if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(row + lane * E);
+            w[0] = x.x, w[1] = x.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(row + lane * E);
+        }
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < W; i++) bits |= not_finite(w[i]) << (2 * i);
+        return bits;
+    };
+    const int64_t ld = (int64_t)sh.Hkv * D;
+    for (int n = first; n <= last; n += gridDim.x) {
+        const Item it = item_of(sh, n);
+        const int tokens = min(2 * sh.nt, sh.Lq - it.i0), rows = tokens * sh.G;
+        const __nv_bfloat16* kb = io.k + ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
+        const __nv_bfloat16* vb = io.v + ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
+        auto at = [&](int r) {
+            return (((size_t)it.b * sh.Lq + it.i0 + r / sh.G) * sh.Hq + it.hk * sh.G + r % sh.G) * D;
+        };
+        auto spoilt = [&](int r, uint32_t (&w)[W]) {
+            const uint32_t bits = dims(io.o + at(r), w);
+            return __shfl_sync(~0u, w[0], 0) == kMeantNan ? 0u : bits;
+        };
+        bool any = false;
+        uint32_t w[W];
+        for (int r = warp; r < rows; r += 4) any |= spoilt(r, w) != 0;
+        if (warp == 0) legit[lane] = 0;
+        if (!outputs_any(any)) continue;
+        // the keys that all of the item's queries see
+        uint32_t bits = 0;
+        const int lo = max(0, it.t0 + tokens - sh.window), sinks = min(sh.n_sink, min(lo, it.t0 + 1));
+        const int common = sinks + max(0, it.t0 + 1 - lo);
+#pragma unroll 4
+        for (int i = warp; i < common; i += 4)
+            bits |= dims(vb + (i < sinks ? i : lo + i - sinks) * ld, w);
+        if (bits) atomicOr(&legit[lane], bits);
+        outputs_any(false);
+        const uint32_t meant = legit[lane];
+        // four rows at a time: they share what they read
+        for (int r0 = warp * R; r0 < rows; r0 += 4 * R) {
+            uint32_t todo[R], left = 0;
+            int t[R];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                todo[r] = r0 + r < rows ? spoilt(r0 + r, w) & ~meant : 0u;
+                t[r] = it.t0 + min(r0 + r, rows - 1) / sh.G;
+                left |= todo[r];
+            }
+            if (!__any_sync(~0u, left)) continue;
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                for (int e = lane; e < D; e += 32)
+                    qf[r * D + e] = __bfloat162float(io.q[at(min(r0 + r, rows - 1)) + e]) * sh.scale2;
+            __syncwarp();
+            const int w0 = max(0, t[0] - sh.window + 1);  // (t - window does not wrap: both are >= 0)
+            const int ns = min(sh.n_sink, w0);
+            float acc[R][E], m[R], l[R];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; e++) acc[r][e] = 0.f;
+            }
+            // 32 keys at a time, the newest first: a lane per key for the logits, the
+            // lane's dims of each key's values for the sums
+            for (int i0 = ns + t[R - 1] - w0; i0 >= 0; i0 -= 32) {
+                const int i = i0 - lane, s = i < 0 ? 0 : i < ns ? i : w0 + i - ns;
+                const uint4* kr = reinterpret_cast<const uint4*>(kb + s * ld);
+                float x[R] = {};
+#pragma unroll 4
+                for (int c = 0; c < D / 8; c++) {
+                    const uint4 z = kr[c];
+                    const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int r = 0; r < R; r++) {
+                        const float* f = qf + r * D + 8 * c;
+#pragma unroll
+                        for (int u = 0; u < 4; u++)
+                            x[r] = fmaf(f[2 * u + 1], bf16_hi(zw[u]), fmaf(f[2 * u], bf16_lo(zw[u]), x[r]));
+                    }
+                }
+                float p[R];  // a weight, or -1 for a key out of the row's sight
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    const bool see = i >= 0 && s <= t[r] && (s > t[r] - sh.window || s < sh.n_sink);
+                    float mn = see ? x[r] : -INFINITY;
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(~0u, mn, off));
+                    mn = fmaxf(m[r], mn);
+                    const bool some = mn > -INFINITY;  // (else no weight yet)
+                    const float a = some ? ex2(m[r] - mn) : 1.f;
+                    p[r] = see ? some ? ex2(x[r] - mn) : 0.f : -1.f;
+                    m[r] = mn;
+                    float sum = fmaxf(p[r], 0.f);
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(~0u, sum, off);
+                    l[r] = fmaf(l[r], a, sum);
+#pragma unroll
+                    for (int e = 0; e < E; e++) acc[r][e] *= a;
+                }
+                __syncwarp();
+                pw[lane] = make_float4(p[0], p[1], p[2], p[3]);
+                __syncwarp();
+                const int keys = min(32, i0 + 1);
+                auto add = [&](int j, bool all) {
+                    dims(vb + __shfl_sync(~0u, s, j) * ld, w);
+                    const float4 pj = pw[j];
+                    const float pr[R] = {pj.x, pj.y, pj.z, pj.w};
+#pragma unroll
+                    for (int r = 0; r < R; r++)
+                        if (all || pr[r] >= 0.f)
+#pragma unroll
+                            for (int e = 0; e < E; e++)
+                                acc[r][e] =
+                                    fmaf(pr[r], e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]), acc[r][e]);
+                };
+                if (__all_sync(~0u, fminf(fminf(p[0], p[1]), fminf(p[2], p[3])) >= 0.f)) {
+#pragma unroll 8
+                    for (int j = 0; j < 32; j++) add(j, true);
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < keys; j++) add(j, false);
+                }
+                bool open = false;
+#pragma unroll
+                for (int r = 0; r < R; r++)
+#pragma unroll
+                    for (int e = 0; e < E; e++) open |= (todo[r] >> e & 1) && acc[r][e] * 0.f == 0.f;
+                if (!__any_sync(~0u, open)) break;
+            }
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float inv = 1.f / l[r];
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    if (todo[r] >> e & 1) io.o[at(r0 + r) + lane * E + e] = __float2bfloat16(acc[r][e] * inv);
+            }
+        }
+        outputs_any(false);  // (all have read `legit`)
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __restrict__ q,
-                   const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse, const Shape sh,
-                   unsigned* __restrict__ flags) {
+window_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Rows io,
+                   const __grid_constant__ Shape sh, unsigned* __restrict__ flags) {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -207,6 +359,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             }
         }
         bars.abort_ = 0;
+        bars.redo_first = INT_MAX, bars.redo_last = -1;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -386,6 +539,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                 const int i = it.i0 + x * sh.nt + tok;
                 const bool real = tok < sh.nt && i < sh.Lq;
                 const float inv = 1.f / ml.y;
+                const bool sane = ml.y > 0.f && ml.y < INFINITY;
                 // NaN once anything is not finite
                 __nv_bfloat162 zero = __float2bfloat162_rn(ml.y * 0.f);
                 const __nv_bfloat162 nought = __float2bfloat162_rn(0.f);
@@ -403,6 +557,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                         p[(u + z) / 2] = *reinterpret_cast<const uint32_t*>(&v);
                     }
                 }
+                if (!sane) p[0] = kMeantNan;
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.o_free[x]);
@@ -422,23 +577,21 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
                         const int r4 = z * 4 + (lane >> 3), to = __shfl_sync(~0u, at, r4);
                         const uint4 v = stage[r4 * 8 + ((lane & 7) ^ (r4 & 7))];
                         if (to >= 0)
-                            *reinterpret_cast<uint4*>(o + (size_t)to * D + u + (lane & 7) * 8) = v;
+                            *reinterpret_cast<uint4*>(io.o + (size_t)to * D + u + (lane & 7) * 8) = v;
                     }
                     __syncwarp();
                 }
-                if (lse && real) lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
+                if (io.lse && real) io.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
                 const bool fine = __low2float(zero) + __high2float(zero) == 0.f;
-                unsigned spoilt = __ballot_sync(~0u, real && !fine);
-                const size_t kv = ((size_t)it.b * sh.Lk * sh.Hkv + it.hk) * D;
-                for (; spoilt; spoilt &= spoilt - 1) {
-                    const int src = __ffs(spoilt) - 1;
-                    const size_t a = __shfl_sync(~0u, at, src);
-                    attend_row<D>(q + a * D, k + kv, v + kv, (int64_t)sh.Hkv * D,
-                                  it.t0 + __shfl_sync(~0u, i, src) - it.i0, sh.window, sh.n_sink,
-                                  sh.scale2, o + a * D, lse ? lse + a : nullptr);
+                if (__any_sync(~0u, real && !fine && sane) && lane == 0) {
+                    atomicMin(&bars.redo_first, w.n);
+                    atomicMax(&bars.redo_last, w.n);
                 }
             }
         }
+        // every product of the CTA has been read by now: its shared memory is free
+        if (!outputs_any(!ok) && bars.redo_last >= 0)
+            redo_items<D>(io, sh, bars.redo_first, bars.redo_last);
     } else {
         // ------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
@@ -461,7 +614,7 @@ window_attn_kernel(const __grid_constant__ Maps maps, const __nv_bfloat16* __res
             const int t_min = it.t0 + x * sh.nt;
             const int all_lo = it.pre - it.base + max(t_min + sh.nt - sh.window, 0);
             const int all_hi = it.pre - it.base + t_min + 1;
-            float m = -1e30f, l = 0.f;
+            float m = -FLT_MAX, l = 0.f;  // (below any finite logit: the first one raises it)
             for (int j = 0; j < it.tiles; j++, c++) {
                 const int e0 = j * BN;
                 const bool second = e0 + 32 < it.entries;  // (else PV reads the first 32 keys at most)
