@@ -1,0 +1,116 @@
+"""GPU tests of the paged decode with value scales that differ widely, against
+the fp64 oracle.
+
+Bounds as in test_gpu_cache_ops.py, but what the kernel drops of a weight is
+counted against what the head's tokens contribute, not against the largest
+scale: at most 2^-28 of the largest (softmax weight) x (V scale) per token, for
+at most 448 of that."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as ora
+from tests.test_gpu_cache_ops import BF, U8, Pool, f64, ints, q_top, status, values
+
+pytestmark = pytest.mark.gpu
+
+
+def check(hs2, pool, q, lengths, window=None, n_sink=0):
+    B, Hq, d = q.shape
+    G = Hq // pool.Hkv
+    scale = 1 / math.sqrt(d)
+    o, lse = hs2.hs2_paged_decode(q, *pool.args(), ints(lengths), window=window, n_sink=n_sink)
+    assert status(hs2) == 0
+    o, lse = f64(o), f64(lse)
+    kv, vv, ks, vs, qa = values(pool.k), values(pool.v), f64(pool.ks), f64(pool.vs), q_top(q, pool.Hkv)
+    q = f64(q)
+    w = 2**31 - 1 if window is None else window
+    for b, T in enumerate(lengths):
+        pos = np.arange(T)
+        pos = pos[(pos >= T - w) | (pos < n_sink)]
+        k, v = (ora.paged_rows(z, s, pool.table_np[b], pool.page, pos) for z, s in ((kv, ks), (vv, vs)))
+        sv = vs[pool.table_np[b][pos // pool.page]]  # [n, Hkv]
+        for h in range(pool.Hkv):
+            at = slice(h * G, (h + 1) * G)
+            r = ora.attend(q[b, at], k[:, h], v[:, h], scale)
+            L = (d + 8) * 2.0**-23 * r["x"] + 2.0**-21 * qa[b, at] * r["k1"]
+            p = np.exp(q[b, at] @ k[:, h].T * scale - r["lse"][:, None])
+            floor = len(pos) * 2.0**-28 * 448 * (p * sv[:, h]).max(1)
+            tol = (2.0**-8 * np.abs(r["o"]) + (2.0**-9 + 2.0**-20 + 4 * L)[:, None] * r["av"] * 1.01
+                   + floor[:, None] + 2.0**-133)
+            err = np.abs(o[b, at] - r["o"])
+            assert np.isfinite(o[b, at]).all() and (err <= tol).all(), float((err / tol).max())
+            tl = L + 2.0**-20 + len(pos) * 2.0**-24 + 2.0**-22 * np.abs(r["lse"])
+            assert (np.abs(lse[b, at] - r["lse"]) <= tl).all()
+
+
+def query(B, Hq, d, seed):
+    return torch.randn(B, Hq, d, generator=torch.Generator().manual_seed(seed)).to(BF).cuda()
+
+
+def aside(pool, pid, octaves):
+    """Pages whose V scale is 2^octaves above the others', which hardly any
+    weight falls on: their keys point away from the queries."""
+    pool.k[pid] = (torch.ones_like(pool.k[pid].float()) * -96).to(torch.float8_e4m3fn).view(U8)
+    pool.ks[pid] = 2.0**-4
+    pool.vs[pid] = 2.0**(octaves - 6)
+
+
+@pytest.mark.parametrize("octaves", [8, 16, 24, 30, 60, 100])
+@pytest.mark.parametrize("G,Hkv,d,page", [(16, 1, 128, 64), (8, 1, 64, 16), (4, 2, 64, 32), (1, 1, 128, 128)])
+def test_large_scales_without_weight_cost_the_others_nothing(cuda_lib, G, Hkv, d, page, octaves):
+    hs2, lengths = cuda_lib, [1500, 9, 700]
+    pool = Pool(3, Hkv, d, page, -(-1500 // page), seed=G).fill(lengths, seed=octaves)
+    pool.vs[pool.table[0].long()] = pool.vs[pool.table[0].long()].clamp(max=2.0**-6)
+    last = (1500 - 1) // page
+    aside(pool, pool.table[0, [0, last // 2, last]].long(), octaves)
+    aside(pool, pool.table[2, :1].long(), octaves)
+    q = query(3, G * Hkv, d, octaves).abs()  # (logits near -6 d / sqrt(d) on the pages set aside)
+    check(hs2, pool, q, lengths)
+    check(hs2, pool, q, lengths, window=300, n_sink=5)
+
+
+@pytest.mark.parametrize("G", [16, 8, 4])
+def test_heads_that_attend_to_pages_of_different_scales(cuda_lib, G):
+    """Half of the heads look at the pages of large values, the others away from
+    them: each head keeps its own pages' bits."""
+    hs2, d, T = cuda_lib, 128, 2000
+    pool = Pool(1, 1, d, 64, 32, seed=2).fill([T], seed=3)
+    pid = pool.table[0].long()
+    big = pid[torch.arange(32, device="cuda") % 3 == 1]
+    pool.vs[pid] = 2.0**-6
+    pool.vs[big] = 2.0**22
+    pool.k[big] = (torch.rand(len(big), 1, 64, d, generator=torch.Generator().manual_seed(1)) * 32 + 64).to(
+        torch.float8_e4m3fn).view(U8).cuda()
+    pool.ks[big] = 2.0**-4
+    q = query(1, G, d, 4).abs()
+    q[:, G // 2:] *= -1
+    check(hs2, pool, q, [T])
+
+
+@pytest.mark.parametrize("low,high", [(-126, -126), (-132, -130), (100, 110), (-126, -40), (-40, 40), (0, 90)])
+def test_scales_of_any_size(cuda_lib, low, high):
+    """All scales tiny (products of codes and scales down to subnormals), all
+    huge, and spread over up to 2^90, rising and falling along the sequence."""
+    hs2, d, T = cuda_lib, 64, 1900
+    for rising in (True, False):
+        pool = Pool(2, 1, d, 32, 60, seed=7).fill([T, 33], seed=8)
+        e = torch.linspace(low, high, 60, device="cuda").round()
+        pid = pool.table.long()
+        pool.vs[pid[0]] = torch.exp2((e if rising else e.flip(0)).double()).float()[:, None]
+        pool.vs[pid[1]] = 2.0**low
+        for g in (3, 16):
+            check(hs2, pool, query(2, g, d, g), [T, 33])
+
+
+def test_parts_of_a_long_sequence_with_uneven_scales(cuda_lib):
+    """Parts on many CTAs, joined: some see large scales without weight only."""
+    hs2, d, T = cuda_lib, 128, 60000
+    pool = Pool(1, 1, d, 128, -(-T // 128), seed=9).fill([T], seed=10)
+    pid = pool.table[0].long()
+    pool.vs[pid] = pool.vs[pid].clamp(max=2.0**-6)
+    aside(pool, pid[100:200], 40)
+    aside(pool, pid[300:310], 90)
+    check(hs2, pool, query(1, 16, d, 5).abs(), [T])

@@ -15,12 +15,15 @@
 //     three e5m2 pieces of 3 bits each: the top bytes of an f16, of its exact
 //     remainder and of 32 times the next.  c's smallest step stands for 2^-21:
 //     smaller weights round to a multiple of it, with the largest weight
-//     kept between 2^8 and 2^14.  (Those six octaves are room for a maximum
+//     kept between 2^7 and 2^14.  (Those octaves are room for a maximum
 //     that grows: with c unscaled and three octaves, a batch with uneven pages
 //     raised its references 13 times per CTA and took 65.0 us, not 62.7.)
 // The pieces are columns of one MMA (N = 2 or 3 times the heads, rounded up to
 // 16) and are summed in fp32.  The page's K scale multiplies the logit, its V
-// scale the weight.
+// scale the weight: w = exp * V scale / C with C a power of two per head that
+// follows the largest product of the two, so that a page of large values that a
+// head does not look at takes no bits from the pages that it does.  The sum of
+// the softmax is of the exponentials alone, in fp32.
 //
 // Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 179 us or
 // 6.0 TB/s, 93% of a copy's rate; 48 ragged sequences with a window of 4096,
@@ -30,6 +33,8 @@
 // copy, 3,500 to its logits, 2,200 for a first reference, 1,400 for weights and
 // outputs, 2,500 for the part's end) and the merge most of the rest.
 #pragma once
+
+#include <float.h>
 
 #include "kv_cache.cuh"
 #include "tc.cuh"
@@ -43,9 +48,10 @@ using kvc::e4m3x2;
 constexpr int kTile = 128;       // tokens per tile
 constexpr int kThreads = 512;    // QK, PV, q, -; four producers; two softmax groups of four
 constexpr int kMaxCtas = 148;    // one per SM
-constexpr float kTopLog2 = 8.f;     // a raised reference maps the largest weight to 2^8
+constexpr float kTopLog2 = 8.f;     // a raised reference maps the largest weight into (2^7, 2^8]
 constexpr float kHalfStep = 2.384185791015625e-7f;  // 2^-22, half of the pieces' smallest step
-constexpr float kRaiseLog2 = 14.f;  // weights above 2^14 (before the V scale) raise it again
+constexpr uint32_t kRaise = 0x7400; // weights above 2^14 (as f16) raise it again,
+constexpr float kRaiseLogit = 60.f; // and so do exponentials above 2^60 (of pages with small scales)
 
 // Scales of pages by their number in the CTA's line of tiles, modulo this: at
 // most 12 stages x 8 pages in flight and two batches of 32 behind them.
@@ -139,7 +145,12 @@ struct Cfg {
     static constexpr int SMEM = OFF_X + NG * D * 4 + 1024;
     static constexpr uint32_t COL_O = 4 * 32;        // S: 4 x 32 columns, O: 2 x 64
     static constexpr int PART = 16 * D + 32;         // floats of a partial result
-    static_assert(SMEM <= 227 * 1024 - 4096, "shared memory");
+};
+
+// A softmax group's references per head, and what a change multiplies its sums
+// and its accumulator by (a copy per warp).
+struct Refs {
+    float R[16], ci[16], down[16], a[16];
 };
 
 struct Bars {
@@ -150,13 +161,16 @@ struct Bars {
     float2 sc[kScRing];     // K and V scale of the line's pages, kAbsent for one not loaded
     float qf[2];            // per item & 1: scale log2(e) over the power of two in q's pieces
     float sqf[4];           // the same per logit buffer
-    float red[2][4][20];    // per group and warp: per-head maxima or sums, largest V scale
+    float red[2][4][32];    // per group and warp and head: maxima of logit and of weight, or sums
     float xr[16], xl[16];
+    alignas(16) Refs refs[2][4];
     Cut cut;
     int n_cta, b0, h0, t0;  // CTAs with tiles; where this one starts
     uint32_t tmem;
     int abort_;
 };
+static_assert(Cfg<128, 16>::SMEM + sizeof(Bars) <= 227 * 1024 && Cfg<64, 16>::SMEM + sizeof(Bars) <= 227 * 1024,
+              "shared memory");
 
 // Shared-memory matrix descriptor with another swizzle than sdesc_sw128's.
 // layout: 0 none, 2 128-byte, 4 64-byte.
@@ -177,6 +191,9 @@ HS2_DEV void mma_f8_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// 1 / x of a power of two in [2^-126, 2^126]
+HS2_DEV float inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
+
 // Barrier of the 128 threads of a softmax group; true if any of them passes true.
 HS2_DEV bool group_any(int group, bool pred) {
     uint32_t r;
@@ -571,15 +588,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         const int g = (warp >> 2) - 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + g * 64;
-        float R[NG], l[NG], vref = 0.f, vinv = 0.f;
+        // exponentials are 2^(logit - R), weights exponential * V scale * ci, ci a
+        // power of two; svlim keeps V scale * ci finite, below svlow it is under 2^-40
+        float R[NG], ci[NG], l[NG], svlim = FLT_MAX, svlow = 0.f;
         int n_x = 0;                  // hand-overs so far
         int st = g, st_was = 0;       // stages of the group's tile and of its last one
         uint32_t ph = 0, ph_was = 0;  // and their barriers' phases
         bool at_start = true;         // the segment begins where the CTA does
         bool from_top = w.t == 0;     // the segment begins where its item does
-        bool has = false, ok = true;  // R and vref are set; no wait has given up
+        bool has = false, ok = true;  // R and ci are set; no wait has given up
 #pragma unroll
-        for (int h = 0; h < NG; h++) R[h] = 0.f, l[h] = 0.f;
+        for (int h = 0; h < NG; h++) R[h] = 0.f, ci[h] = 1.f, l[h] = 0.f;
 
         for (int i0 = 0; i0 < n_tiles;) {
             const int n = min(w.s.tiles - w.t, n_tiles - i0);  // tiles of the segment
@@ -603,50 +622,84 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.s_empty[sb]);
-                float y[NG], top = -INFINITY;
+                // exponentials, and weights: nine significant bits, and no step below
+                // 2^-21: half a step of each added, what is below it cut
+                float y[NG], p[NG];
+                uint32_t pc[NG / 2], top = 0;
+                auto weigh = [&]() {
+                    const float svc = fminf(sv, svlim);
+#pragma unroll
+                    for (int h = 0; h < NG; h += 2) {
+                        p[h] = vis ? ex2(y[h]) : 0.f;
+                        p[h + 1] = vis ? ex2(y[h + 1]) : 0.f;
+                        pc[h / 2] = pack_f16(fmaf(p[h], svc * ci[h], kHalfStep),
+                                             fmaf(p[h + 1], svc * ci[h + 1], kHalfStep));
+                    }
+                };
 #pragma unroll
                 for (int h = 0; h < NG; h++) {
                     const float x = fmaf(__uint_as_float(r[NG + h]), 0.0625f, __uint_as_float(r[h]));
                     y[h] = fmaf(x, f, -R[h]);
-                    top = fmaxf(top, y[h]);
                 }
-                const bool raise = vis && (!has || top > kRaiseLog2 || sv > 2.f * vref);
-                if (group_any(g, raise || !ok)) {
-                    // a new reference (the segment's first tile, or a larger weight)
+                weigh();
+                // (non-negative: their bits order as they do)
+#pragma unroll
+                for (int h = 0; h < NG / 2; h++) top = __vmaxu2(top, pc[h]);
+                bool raise = !has || max(top & 0xFFFFu, top >> 16) > kRaise;
+                if (vis && sv < svlow) {  // (weights too small to tell how large the exponentials are)
+#pragma unroll
+                    for (int h = 0; h < NG; h++) raise |= y[h] > kRaiseLogit;
+                }
+                if (group_any(g, (raise && vis) || !ok)) {
+                    // new references (the segment's first tile, or a larger weight)
                     if (j > 1) ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
                     fence_after_sync();
+                    // the tile's largest logit and largest log2 of exponential * V scale
+                    const float lsv = vis ? __log2f(sv) : -INFINITY;
 #pragma unroll
                     for (int h = 0; h < NG; h++) {
-                        float x = vis ? y[h] + R[h] : -INFINITY;
-                        x = warp_max(x);
-                        if (lane == 0) bars.red[g][wq][h] = x;
+                        const float x = vis ? y[h] + R[h] : -INFINITY;
+                        const float xm = warp_max(x), zm = warp_max(x + lsv);
+                        if (lane == 0) bars.red[g][wq][h] = xm, bars.red[g][wq][NG + h] = zm;
                     }
-                    const float sm = __uint_as_float(
-                        __reduce_max_sync(~0u, __float_as_uint(fmaxf(sv, 0.f))));
-                    if (lane == 0) bars.red[g][wq][16] = sm;
                     if (group_any(g, !ok)) {
                         ok = false;
                         break;
                     }
-                    float vnew = vref;
+                    // each warp for itself, a lane per head
+                    Refs& refs = bars.refs[g][wq];
+                    {
+                        const int h = lane % NG;
+                        float xm = bars.red[g][0][h], zm = bars.red[g][0][NG + h];
 #pragma unroll
-                    for (int u = 0; u < 4; u++) vnew = fmaxf(vnew, 2.f * bars.red[g][u][16]);
-                    const float beta = vnew > 0.f ? vref / vnew : 0.f;
-                    vref = vnew;
-                    vinv = vnew > 0.f ? 1.f / vnew : 0.f;
-                    float a[NG];
-#pragma unroll
-                    for (int h = 0; h < NG; h++) {
-                        float m = bars.red[g][0][h];
-#pragma unroll
-                        for (int u = 1; u < 4; u++) m = fmaxf(m, bars.red[g][u][h]);
-                        const float Rn = has ? fmaxf(R[h], m - kTopLog2) : m - kTopLog2;
-                        a[h] = has ? ex2(R[h] - Rn) : 0.f;
-                        y[h] += R[h] - Rn;
-                        R[h] = Rn;
-                        l[h] *= a[h];
+                        for (int u = 1; u < 4; u++) {
+                            xm = fmaxf(xm, bars.red[g][u][h]);
+                            zm = fmaxf(zm, bars.red[g][u][NG + h]);
+                        }
+                        // (whole numbers: every rescaling is by a power of two)
+                        xm = ceilf(xm) - kTopLog2;
+                        const float Ro = has ? refs.R[h] : xm, co = has ? refs.ci[h] : 0x1p126f;
+                        float Rn = fmaxf(Ro, xm);
+                        if (Rn == -INFINITY) Rn = 0.f;  // (logits of NaN alone)
+                        const float e = fminf(fmaxf(Rn + kTopLog2 - ceilf(zm), -126.f), 126.f);
+                        const float cn = fminf(__uint_as_float((uint32_t)((int)e + 127) << 23),
+                                               co * ex2(fminf(Rn - Ro, 126.f)));
+                        const float down = has ? ex2(Ro - Rn) : 0.f;
+                        svlim = inverse(warp_max(cn)) * 0x1p126f * 2.f;  // (at most infinity)
+                        svlow = inverse(-warp_max(-cn)) * 0x1p-40f;
+                        __syncwarp();
+                        refs.R[h] = Rn, refs.ci[h] = cn, refs.down[h] = down;
+                        refs.a[h] = cn * down * inverse(co);
+                        __syncwarp();
                     }
                     has = true;
+#pragma unroll
+                    for (int h = 0; h < NG; h++) {
+                        y[h] += R[h] - refs.R[h];
+                        R[h] = refs.R[h];
+                        ci[h] = refs.ci[h];
+                        l[h] *= refs.down[h];
+                    }
                     if (j > 1) {
 #pragma unroll 1
                         for (int c = 0; c < C::NP; c += 16) {
@@ -655,26 +708,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                             tmem_ld_wait();
 #pragma unroll
                             for (int u = 0; u < 16; u++)
-                                v[u] = __float_as_uint(__uint_as_float(v[u]) *
-                                                       (a[u % NG] * beta));
+                                v[u] = __float_as_uint(__uint_as_float(v[u]) * refs.a[u % NG]);
                             tmem_st16(o_col + c, v);
                         }
                         tmem_st_wait();
                     }
                     fence_before_sync();
+                    weigh();
                 }
-                // weights, their sums and their pieces
-                const float rv = sv * vinv;
-                uint32_t pc[NG / 2];
+                // the exponentials' sums, and the weights' pieces
 #pragma unroll
                 for (int h = 0; h < NG; h += 2) {
-                    const float p0 = vis ? ex2(y[h]) : 0.f, p1 = vis ? ex2(y[h + 1]) : 0.f;
-                    l[h] += p0;
-                    l[h + 1] += p1;
-                    // nine significant bits, and no step below 2^-21: half a step of
-                    // each added, what is below it cut
-                    pc[h / 2] = (pack_f16(fmaf(p0, rv, kHalfStep), fmaf(p1, rv, kHalfStep)) + 0x00020002u) &
-                                0xFFFCFFFCu;
+                    l[h] += p[h];
+                    l[h + 1] += p[h + 1];
+                    pc[h / 2] = (pc[h / 2] + 0x00020002u) & 0xFFFCFFFCu;
                 }
                 uint32_t b1[NG / 4], b2[NG / 4], b3[NG / 4];
 #pragma unroll
@@ -697,16 +744,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     b3[j] = prmt(x0, x1, 0x7531u);
                 }
                 if (k > 0) ok = ok && mbar_wait(&bars.empty[st_was], ph_was, abort_, flags);
-                uint8_t* p = smem + C::OFF_P + g * C::PB + row * 16;
+                uint8_t* pp = smem + C::OFF_P + g * C::PB + row * 16;
                 if constexpr (NG == 16) {
-                    *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
-                    *reinterpret_cast<uint4*>(p + kTile * 16) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
-                    *reinterpret_cast<uint4*>(p + kTile * 32) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
+                    *reinterpret_cast<uint4*>(pp) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
+                    *reinterpret_cast<uint4*>(pp + kTile * 16) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
+                    *reinterpret_cast<uint4*>(pp + kTile * 32) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
                 } else if constexpr (NG == 8) {
-                    *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b1[1], b2[0], b2[1]);
-                    *reinterpret_cast<uint4*>(p + kTile * 16) = make_uint4(b3[0], b3[1], 0u, 0u);
+                    *reinterpret_cast<uint4*>(pp) = make_uint4(b1[0], b1[1], b2[0], b2[1]);
+                    *reinterpret_cast<uint4*>(pp + kTile * 16) = make_uint4(b3[0], b3[1], 0u, 0u);
                 } else {
-                    *reinterpret_cast<uint4*>(p) = make_uint4(b1[0], b2[0], b3[0], 0u);
+                    *reinterpret_cast<uint4*>(pp) = make_uint4(b1[0], b2[0], b3[0], 0u);
                 }
                 if (!vis) {
                     // 0 * NaN is NaN: a row that is not visible must not hold one
@@ -774,10 +821,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 fence_before_sync();
 #pragma unroll
                 for (int h = 0; h < NG; h++) {
-                    O[h] *= vref;
                     l[h] = 0.f;
 #pragma unroll
                     for (int u = 0; u < 4; u++) l[h] += bars.red[g][u][h];
+                    // over the power of two in l, so that O is at most twice the
+                    // segment's largest value (division by l itself: 2 us more)
+                    const uint32_t two = __float_as_uint(l[h]) & 0x7F800000u;
+                    const float ln = __uint_as_float((254u << 23) - two);
+                    O[h] = O[h] * ln * inverse(ci[h]);
+                    l[h] *= ln;
+                    R[h] += (float)((int)(two >> 23) - 127);
                     if (!has) R[h] = -1e30f;  // nothing visible: no weight when merged
                 }
                 float* xo = reinterpret_cast<float*>(smem + C::OFF_X);
@@ -835,8 +888,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 }
                 if (both) n_x++;
 #pragma unroll
-                for (int h = 0; h < NG; h++) R[h] = 0.f, l[h] = 0.f;
-                vref = vinv = 0.f;
+                for (int h = 0; h < NG; h++) R[h] = 0.f, ci[h] = 1.f, l[h] = 0.f;
+                svlim = FLT_MAX, svlow = 0.f;
                 has = false;
                 }
             at_start = false;
