@@ -515,7 +515,10 @@ def _dense(t, name: str, dtypes, shape, dev: int):
     try:
         if (t.dtype in dtypes and t.shape == shape and t.is_contiguous()
                 and t.get_device() == dev):
-            return t.data_ptr()
+            p = t.data_ptr()
+            if p & 15:
+                raise ValueError(f"{name}: must start on a 16-byte boundary (a slice of a larger tensor? copy it)")
+            return p
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor):
