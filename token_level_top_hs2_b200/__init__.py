@@ -509,6 +509,12 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _INT_MAX = 2**31 - 1
 
 
+def _c_int(x) -> int:
+    """x as a C int: above its range the largest one, below -1, which is refused
+    (ctypes would wrap)."""
+    return max(-1, min(x, _INT_MAX))
+
+
 def _dense(t, name: str, dtypes, shape, dev: int):
     """Device pointer of a dense tensor of exactly this shape on device `dev`
     (the checks of _ptr, with the shape instead of the element count)."""
@@ -687,7 +693,7 @@ def hs2_paged_decode(q, k_pages, v_pages, k_scale, v_scale, table, lengths, *, w
                     getattr(workspace, "shape", None), dev)
         n_ws = workspace.numel() * workspace.element_size()
     st = load().hs2_paged_decode(
-        shape, Hq, _INT_MAX if window is None else min(window, _INT_MAX), min(n_sink, _INT_MAX),
+        shape, Hq, _INT_MAX if window is None else _c_int(window), _c_int(n_sink),
         1.0 / math.sqrt(d) if scale is None else float(scale), _dense(q, "q", _BF16, out, dev), *ptrs,
         _dense(lengths, "lengths", _I32, (shape.B,), dev), _dense(o, "o", _BF16, out, dev),
         _dense_or_none(lse, "lse", _F32, out[:2], dev), ws, n_ws, _raw_stream(stream, dev))
@@ -707,7 +713,7 @@ def hs2_window_attn(q, k, v, window: int, n_sink: int = 0, *, scale=None, o=None
     o = _alloc(stream, rows, torch.bfloat16, dev) if o is None else o
     if lse is None and want_lse:
         lse = _alloc(stream, rows[:3], torch.float32, dev)
-    shape = _window_shape(B, Lq, Lk, Hq, Hkv, d, min(window, _INT_MAX), min(n_sink, _INT_MAX),
+    shape = _window_shape(B, Lq, Lk, Hq, Hkv, d, _c_int(window), _c_int(n_sink),
                           1.0 / math.sqrt(d) if scale is None else float(scale))
     st = load().hs2_window_attn(
         shape, _dense(q, "q", _BF16, rows, dev), _dense(k, "k", _BF16, keys, dev),
