@@ -15,15 +15,16 @@
 //     three e5m2 pieces of 3 bits each: the top bytes of an f16, of its exact
 //     remainder and of 32 times the next.  c's smallest step stands for 2^-21:
 //     smaller weights round to a multiple of it, with the largest weight
-//     kept between 2^7 and 2^14.  (Those octaves are room for a maximum
+//     kept between 2^8 and 2^14.  (Those six octaves are room for a maximum
 //     that grows: with c unscaled and three octaves, a batch with uneven pages
 //     raised its references 13 times per CTA and took 65.0 us, not 62.7.)
 // The pieces are columns of one MMA (N = 2 or 3 times the heads, rounded up to
 // 16) and are summed in fp32.  The page's K scale multiplies the logit, its V
-// scale the weight: w = exp * V scale / C with C a power of two per head that
-// follows the largest product of the two, so that a page of large values that a
-// head does not look at takes no bits from the pages that it does.  The sum of
-// the softmax is of the exponentials alone, in fp32.
+// scale the weight: w = exp * V scale / C with a C per head that follows the
+// largest product of the two, so that a page of large values that a head does
+// not look at takes no bits from the pages that it does.  The token that sets C
+// has the weight 2^8 exactly: a sharp softmax keeps its largest weight whole.
+// The sum of the softmax is of the exponentials alone, in fp32.
 //
 // Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 179 us or
 // 6.0 TB/s, 93% of a copy's rate; 48 ragged sequences with a window of 4096,
@@ -48,7 +49,7 @@ using kvc::e4m3x2;
 constexpr int kTile = 128;       // tokens per tile
 constexpr int kThreads = 512;    // QK, PV, q, -; four producers; two softmax groups of four
 constexpr int kMaxCtas = 148;    // one per SM
-constexpr float kTopLog2 = 8.f;     // a raised reference maps the largest weight into (2^7, 2^8]
+constexpr float kTopLog2 = 8.f;     // a raised reference maps the largest weight to 2^8
 constexpr float kHalfStep = 2.384185791015625e-7f;  // 2^-22, half of the pieces' smallest step
 constexpr uint32_t kRaise = 0x7400; // weights above 2^14 (as f16) raise it again,
 constexpr float kRaiseLogit = 60.f; // and so do exponentials above 2^60 (of pages with small scales)
@@ -164,6 +165,7 @@ struct Bars {
     float red[2][4][32];    // per group and warp and head: maxima of logit and of weight, or sums
     float xr[16], xl[16];
     alignas(16) Refs refs[2][4];
+    float C[2][16];         // per group and head: 1 / ci
     Cut cut;
     int n_cta, b0, h0, t0;  // CTAs with tiles; where this one starts
     uint32_t tmem;
@@ -191,7 +193,7 @@ HS2_DEV void mma_f8_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// 1 / x of a power of two in [2^-126, 2^126]
+// 1 / x of an x in [2^-126, 2^126], up to an eighth more
 HS2_DEV float inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // Barrier of the 128 threads of a softmax group; true if any of them passes true.
@@ -588,8 +590,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         const int g = (warp >> 2) - 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t o_col = lanes + C::COL_O + g * 64;
-        // exponentials are 2^(logit - R), weights exponential * V scale * ci, ci a
-        // power of two; svlim keeps V scale * ci finite, below svlow it is under 2^-40
+        // rounds two f16 to nine significant bits: halves go up at even tokens and
+        // down at odd ones (all up, outputs came out 2^-11.5 too large)
+        const uint32_t nine = lane & 1 ? 0x00010001u : 0x00020002u;
+        // exponentials are 2^(logit - R), weights exponential * V scale * ci; svlim
+        // keeps V scale * ci finite, below svlow it may be under 2^-40
         float R[NG], ci[NG], l[NG], svlim = FLT_MAX, svlow = 0.f;
         int n_x = 0;                  // hand-overs so far
         int st = g, st_was = 0;       // stages of the group's tile and of its last one
@@ -676,20 +681,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                             xm = fmaxf(xm, bars.red[g][u][h]);
                             zm = fmaxf(zm, bars.red[g][u][NG + h]);
                         }
-                        // (whole numbers: every rescaling is by a power of two)
-                        xm = ceilf(xm) - kTopLog2;
-                        const float Ro = has ? refs.R[h] : xm, co = has ? refs.ci[h] : 0x1p126f;
+                        xm -= kTopLog2;
+                        const float Ro = has ? refs.R[h] : xm, co = has ? refs.ci[h] : 0x1p125f;
                         float Rn = fmaxf(Ro, xm);
                         if (Rn == -INFINITY) Rn = 0.f;  // (logits of NaN alone)
-                        const float e = fminf(fmaxf(Rn + kTopLog2 - ceilf(zm), -126.f), 126.f);
-                        const float cn = fminf(__uint_as_float((uint32_t)((int)e + 127) << 23),
-                                               co * ex2(fminf(Rn - Ro, 126.f)));
+                        const float e = fminf(fmaxf(Rn + kTopLog2 - zm, -125.f), 125.f);
+                        const float cn = fminf(ex2(e), co * ex2(fminf(Rn - Ro, 125.f)));
                         const float down = has ? ex2(Ro - Rn) : 0.f;
                         svlim = inverse(warp_max(cn)) * 0x1p126f * 2.f;  // (at most infinity)
                         svlow = inverse(-warp_max(-cn)) * 0x1p-40f;
                         __syncwarp();
                         refs.R[h] = Rn, refs.ci[h] = cn, refs.down[h] = down;
-                        refs.a[h] = cn * down * inverse(co);
+                        refs.a[h] = __fdividef(cn * down, co);
+                        bars.C[g][h] = __fdividef(1.f, cn);  // (the same from every warp)
                         __syncwarp();
                     }
                     has = true;
@@ -721,7 +725,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                 for (int h = 0; h < NG; h += 2) {
                     l[h] += p[h];
                     l[h + 1] += p[h + 1];
-                    pc[h / 2] = (pc[h / 2] + 0x00020002u) & 0xFFFCFFFCu;
+                    pc[h / 2] = (pc[h / 2] + nine) & 0xFFFCFFFCu;
                 }
                 uint32_t b1[NG / 4], b2[NG / 4], b3[NG / 4];
 #pragma unroll
@@ -828,7 +832,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                     // segment's largest value (division by l itself: 2 us more)
                     const uint32_t two = __float_as_uint(l[h]) & 0x7F800000u;
                     const float ln = __uint_as_float((254u << 23) - two);
-                    O[h] = O[h] * ln * inverse(ci[h]);
+                    O[h] = has ? O[h] * ln * bars.C[g][h] : 0.f;
                     l[h] *= ln;
                     R[h] += (float)((int)(two >> 23) - 127);
                     if (!has) R[h] = -1e30f;  // nothing visible: no weight when merged
