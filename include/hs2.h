@@ -353,7 +353,8 @@ hs2_status hs2_kv_read(const hs2_cache_shape* shape, int N, const void* k_cache,
  * of two >= 2^-126 with max|x| <= 448 p over those rows.  A page whose first
  * row the call writes gets scale p.  A page that holds earlier rows keeps its
  * scale s if s >= p; otherwise its scale becomes p and the earlier rows' codes
- * become e4m3(code * s / p).  Then code = e4m3(x / scale).  A page's rows
+ * become e4m3(code * s / p).  Then code = e4m3(x / scale), the quotient in
+ * fp32 (an earlier scale need not be a power of two).  A page's rows
  * behind the last one written hold nothing: a later call may write them.  The
  * pages that one call writes must be distinct (a page shared by sequences is
  * for reading).  Infinities and NaN as in hs2_kv_write; an earlier scale that

@@ -289,6 +289,18 @@ paged_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16*
             *reinterpret_cast<uint2*>(dst + (size_t)unit * 8) = make_uint2(c0 | c1 << 16, c2 | c3 << 16);
         }
     }
+    if (__float_as_uint(s) & 0x7FFFFFu) {
+        // no power of two, so the reciprocal is not exact: a page that another
+        // writer began.  Its rows are read again and divided (a division in the
+        // loop above costs every call: 604 MB in 146 us, not 102)
+#pragma unroll 1
+        for (int unit = tid; unit < p1 * LPR; unit += kPageThreads) {  // (the same thread's as above)
+            if (unit / LPR < p0) continue;
+            const size_t i = (size_t)b * N + (first + unit / LPR);
+            const uint4 x = ldg_stream(src + (i * Hkv + h) * D + (unit % LPR) * 8);
+            *reinterpret_cast<uint2*>(dst + (size_t)unit * 8) = quantise8(x, s, 1.f, false);
+        }
+    }
     if (tid == 0) *scale = s;
     if (bad) atomicOr(flags, FLAG_NONFINITE);
 }
