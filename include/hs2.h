@@ -381,9 +381,9 @@ hs2_status hs2_paged_kv_read(const hs2_paged_shape* shape, int N, const void* k_
  *            outputs of their KV head's query heads mean nothing
  *   k_pages, v_pages, k_scale, v_scale: scales finite and > 0, V scales at most
  *            2^110.  Of a token whose softmax weight times V scale is less than
- *            2^-28 of the largest such product of its query head nothing is kept
- *            (an error of at most 448 times that per token); this holds for V
- *            scales within 2^100 of one another, pages of zeros aside
+ *            2^-28 of the largest such product of its query head, or 2^-60 of the
+ *            largest V scale in sight, nothing need be kept (an error of at most
+ *            448 times that per token)
  *   lengths  [B] int32, device, each in [0, max_pages * page]; a length of 0
  *            gives o = 0 and lse = -inf, one out of range the same and a flag
  *   o        [B, Hq, d] bf16 out;  lse [B, Hq] fp32 out (natural log), may be NULL

@@ -145,3 +145,30 @@ def test_the_largest_weight_stays_whole_and_the_others_unbiased(cuda_lib):
     want = torch.from_numpy(values(pool.v)[pid, 0, 5] * float(pool.vs[pid, 0])).to(BF)
     assert s < T and status(hs2) == 0
     assert torch.equal(o.cpu(), want.expand(1, G, d))
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("G,d,page", [(16, 128, 64), (8, 128, 32), (4, 128, 16)])
+def test_heads_that_look_at_a_page_of_zeros_alone(cuda_lib, G, d, page, first):
+    """Half of the heads at a page of zeros (scale 2^-126), 100 nats above all
+    else, the others at values of thousands: these are right, and those are what
+    is left, next to nothing."""
+    hs2, T = cuda_lib, 1500
+    mp = -(-T // page)
+    pool = Pool(1, 1, d, page, mp, seed=18).fill([T], seed=19)
+    pid = pool.table[0].long()
+    pool.vs[pid] = 2.0**6
+    pool.ks[pid] = 2.0**-4
+    pool.k[pid] = 0x80 | 0x6C                 # -96
+    zero = pid[0 if first else mp - 1]
+    pool.k[zero] = 0x6C
+    pool.v[zero], pool.vs[zero] = 0, 2.0**-126
+    q = query(1, G, d, 20).abs()
+    q[:, 1::2] *= -1
+    o, lse = hs2.hs2_paged_decode(q, *pool.args(), ints([T]))
+    assert status(hs2) == 0
+    r = pool.oracle(q, [T], 2**31 - 1, 0, 1 / math.sqrt(d))
+    tol = (2.0**-8 * np.abs(r["o"]) + (2.0**-9 + 2.0**-10) * r["av"])[:, 1::2]
+    assert (np.abs(f64(o) - r["o"])[:, 1::2] <= tol).all()
+    assert (np.abs(f64(o) - r["o"])[:, ::2] <= 2.0**-60 * 2.0**6 * 448).all()
+    np.testing.assert_allclose(f64(lse), r["lse"], rtol=2.0**-20, atol=2.0**-10)

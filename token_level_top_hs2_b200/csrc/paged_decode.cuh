@@ -686,10 +686,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                         float Rn = fmaxf(Ro, xm);
                         if (Rn == -INFINITY) Rn = 0.f;  // (logits of NaN alone)
                         const float e = fminf(fmaxf(Rn + kTopLog2 - zm, -125.f), 125.f);
-                        const float cn = fminf(ex2(e), co * ex2(fminf(Rn - Ro, 125.f)));
+                        float cn = fminf(ex2(e), co * ex2(fminf(Rn - Ro, 125.f)));
+                        // at most 2^60 apart, so that svlim touches only tokens that
+                        // contribute less than 2^-67 of their V scale to any head (a
+                        // head may look at a page of zeros alone, whose scale is 2^-126)
+                        const float least = -warp_max(-cn);
+                        cn = fminf(cn, least * 0x1p60f);
                         const float down = has ? ex2(Ro - Rn) : 0.f;
                         svlim = inverse(warp_max(cn)) * 0x1p126f * 2.f;  // (at most infinity)
-                        svlow = inverse(-warp_max(-cn)) * 0x1p-40f;
+                        svlow = inverse(least) * 0x1p-40f;
                         __syncwarp();
                         refs.R[h] = Rn, refs.ci[h] = cn, refs.down[h] = down;
                         refs.a[h] = __fdividef(cn * down, co);
