@@ -409,8 +409,11 @@ hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, in
  *   q [B, Lq, Hq, d] bf16, k, v [B, Lk, Hkv, d] bf16; Hq a multiple of Hkv, at
  *   most 16 query heads per KV head (query head h reads KV head h / (Hq / Hkv))
  *   o [B, Lq, Hq, d] bf16 out; lse [B, Lq, Hq] fp32 out (natural log), may be NULL
+ *   o must not overlap q, k or v
  * A row that a query does not see never reaches its output, whatever it holds
- * (the padding of a right-padded batch may be anything).
+ * (the padding of a right-padded batch may be anything).  A call's work is cut
+ * by 2 floor(128 / (Hq / Hkv)) queries of a KV head, not along the keys: few
+ * queries of few sequences over a long cache leave most of the GPU idle.
  */
 typedef struct {
     int B, Lq, Lk, Hq, Hkv, d, window, n_sink;

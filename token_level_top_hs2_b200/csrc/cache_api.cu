@@ -331,9 +331,12 @@ hs2_status hs2_paged_decode(const hs2_paged_shape* shape, int Hq, int window, in
     const PagedCall c = {shape, q, k_pages, v_pages, k_scale, v_scale, table, lengths,
                          o,     lse, static_cast<float*>(workspace), Hq / shape->Hkv, window, n_sink,
                          scale, st, flags};
-    // a thread's exponentials and registers go by the heads it is built for: 48
-    // ragged sequences of 8 KV heads of 64 with groups of four took 55.4 us built
-    // for four heads, 63.3 for eight and 86.1 for sixteen
+    // a thread's exponentials and registers go by the heads it is built for.  48
+    // ragged sequences of 8 KV heads: groups of four, heads of 64, 53.1 us built
+    // for four against 59.9 for eight; heads of 128, 77.4 against 79.0; groups of
+    // eight, 62.5 built for eight against 86.7 for sixteen; 81.2 against 92.5.
+    // 8 sequences of 60k tokens, 4 KV heads of 128: groups of four 55.2 against
+    // 56.5, of eight 56.4 against 62.9
     if (shape->d == 128)
         return c.G > 8 ? run_paged<128, 16>(c) : c.G > 4 ? run_paged<128, 8>(c) : run_paged<128, 4>(c);
     return c.G > 8 ? run_paged<64, 16>(c) : c.G > 4 ? run_paged<64, 8>(c) : run_paged<64, 4>(c);

@@ -94,8 +94,9 @@ HS2_DEV uint2 quantise8(uint4 w, float s, float r, bool finite) {
 
 // One group of D/16 lanes per row, sixteen elements of K and of V a lane (the
 // row's maximum, its scale and the reciprocal are the lanes' common cost: with
-// eight elements 128k rows of 128 took 24.6 us, now 22.2: 4.6 TB/s, bound by
-// the issue of instructions).  grid (rows, B).
+// eight elements 128k rows of 128 took 24.6 us, now 22.2: 4.6 TB/s, with 67% of
+// the issue slots in use; short blocks whose loads only other blocks cover).
+// grid (rows, B).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 token_write_kernel(const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new,
@@ -159,7 +160,8 @@ HS2_DEV uint2 ldg_stream8(const void* p) {
 
 // Eight codes a lane, so that a warp's stores are whole 512-byte runs.  38.5 MB
 // (4 sequences of 16-32k rows of 64) in 10.3 us, of which the bytes need 6 and
-// the launch most of the rest.  grid (rows, B).
+// the launch most of the rest; 407 MB (512k rows of 128) in 65.7 us, 6.2 TB/s.
+// grid (rows, B).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 token_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
@@ -202,8 +204,8 @@ token_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict
 // One block per (touched page, KV head, K or V) and sequence; the page's new
 // rows stay in registers between the search for their largest magnitude and
 // the rounding, so they are read once.  604 MB (4 sequences of 16-32k rows, 8
-// heads of 128) in 101.7 us, 5.9 TB/s: bound by the memory.  grid (pages * Hkv *
-// 2, B).
+// heads of 128) in 98 to 108 us, 5.6 to 6.2 TB/s: bound by the memory.  grid
+// (pages * Hkv * 2, B).
 constexpr int kPageThreads = 128;
 
 template <int D, int PAGE>

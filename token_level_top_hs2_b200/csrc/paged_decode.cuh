@@ -11,7 +11,8 @@
 //     each after a common power of two per KV head that puts max|q| in
 //     [128, 256).  Exact for every element above 2^-14 of the largest; below,
 //     the error is at most 2^-21 of the largest.
-//   * a weight w (nine significant bits, rounded to nearest) = a + b + c / 32,
+//   * a weight w (nine significant bits, one more than a bf16 output has) =
+//     a + b + c / 32,
 //     three e5m2 pieces of 3 bits each: the top bytes of an f16, of its exact
 //     remainder and of 32 times the next.  c's smallest step stands for 2^-21:
 //     smaller weights round to a multiple of it, with the largest weight
@@ -26,13 +27,14 @@
 // has the weight 2^8 exactly: a sharp softmax keeps its largest weight whole.
 // The sum of the softmax is of the exponentials alone, in fp32.
 //
-// Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 179 us or
-// 6.0 TB/s, 93% of a copy's rate; 48 ragged sequences with a window of 4096,
-// 8 KV heads of 64 and groups of four (202 MB), 53.5 us or 3.8 TB/s, bound by
-// the softmax warps' latency per tile; one sequence of 1k tokens 12.4 us, of
-// which 7 are one tile's way through the kernel (13k cycles: 3,500 to the first
-// copy, 3,500 to its logits, 2,200 for a first reference, 1,400 for weights and
-// outputs, 2,500 for the part's end) and the merge most of the rest.
+// Measured: 16 sequences of 256k tokens, 16 heads of 128 (1.07 GB), 179 to 185
+// us in a burst of calls (5.8 to 6.0 TB/s, 90 to 93% of a copy's rate), 207 over
+// seconds at the power cap (5.2 TB/s, 80%); 48 ragged sequences with a window of
+// 4096, 8 KV heads of 64 and groups of four (202 MB), 53.1 us either way or 3.8
+// TB/s, bound by the softmax warps' latency per tile; one sequence of 1k tokens
+// 12.4 us, of which 7 are one tile's way through the kernel (13k cycles: 3,500
+// to the first copy, 3,500 to its logits, 2,200 for a first reference, 1,400 for
+// weights and outputs, 2,500 for the part's end) and the merge most of the rest.
 #pragma once
 
 #include <float.h>

@@ -22,14 +22,20 @@
 //               at the end, rows that masked NaN or infinities have spoilt
 //   warps 8-11  softmax of tile 0, thread = row = TMEM lane
 //   warps 12-15 softmax of tile 1
-// P (bf16, as V is) overwrites its logits; the running maximum is raised only
-// when a tile exceeds it by 2^8, so the accumulator is rarely rescaled.
+// P overwrites its logits, rounded to bf16 since both operands of the product
+// have V's type (the sum is of the unrounded weights: outputs are off by 0.0021
+// to 0.0023 of their size where a bf16 output alone is by 0.0017); the running
+// maximum is raised only when a tile exceeds it by 2^8, so the accumulator is
+// rarely rescaled.
 //
-// Measured: 128k queries of 16 heads of 128, window 128 (1.15 GB), 246 us or
-// 4.67 TB/s, bound by the chain of an item's softmax steps (most of its tiles
+// Measured: 128k queries of 16 heads of 128, window 128 (1.15 GB), 243 to 253
+// us in a burst of calls (4.5 to 4.7 TB/s), 300 over seconds at the power cap
+// (3.8 TB/s), bound by the chain of an item's softmax steps (most of its tiles
 // of keys are partly masked); 2 x 16k queries of 32 heads in 8 groups, window
-// 4096 (2.16 TF), 2.0 ms or 1.07 PF/s at the power cap, 55% of the tensor
-// pipe's cycles, bound by exponentials and power.
+// 4096 (2.16 TF), 1.86 to 2.07 ms in a burst, 2.14 over seconds (1.0 PF/s), 55% of
+// the tensor pipe's cycles, bound by exponentials and power.  An item's keys are
+// not split: with fewer items than SMs the longest one is the call's time, 69 us
+// for one query of 16 heads over 4,096 keys, 1.48 ms over 100,000.
 #pragma once
 
 #include <float.h>
