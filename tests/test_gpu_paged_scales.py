@@ -172,3 +172,44 @@ def test_heads_that_look_at_a_page_of_zeros_alone(cuda_lib, G, d, page, first):
     assert (np.abs(f64(o) - r["o"])[:, 1::2] <= tol).all()
     assert (np.abs(f64(o) - r["o"])[:, ::2] <= 2.0**-60 * 2.0**6 * 448).all()
     np.testing.assert_allclose(f64(lse), r["lse"], rtol=2.0**-20, atol=2.0**-10)
+
+
+@pytest.mark.parametrize("G", [16, 8, 3])
+@pytest.mark.parametrize("rising", [True, False])
+def test_logits_far_apart_on_pages_of_zeros(cuda_lib, G, rising):
+    """Logits that rise or fall by 160 nats along pages of zeros, whose weights
+    are too small to show it, in front of ordinary pages at the height of the top."""
+    hs2, d, page, T = cuda_lib, 128, 64, 31 * 64
+    mp = T // page
+    pool = Pool(1, 1, d, page, mp, seed=21).fill([T], seed=22)
+    pid, zeros = pool.table[0].long(), mp - 4
+    x = torch.linspace(-80, 80, zeros * page).view(zeros, 1, page, 1).expand(zeros, 1, page, d)
+    x = (x if rising else x.flip(0, 2)) / math.sqrt(d) * 2**4
+    pool.k[pid[:zeros]] = x.to(torch.float8_e4m3fn).view(U8).cuda()
+    pool.ks[pid] = 2.0**-4
+    pool.v[pid[:zeros]], pool.vs[pid[:zeros]] = 0, 2.0**-126
+    pool.k[pid[zeros:]] = torch.tensor(80 / math.sqrt(d) * 2**4).to(torch.float8_e4m3fn).view(U8).cuda()
+    for order in (pid, pid.flip(0)):
+        pool.table[0] = order.int()
+        pool.table_np = pool.table.cpu().numpy()
+        check(hs2, pool, torch.ones(1, G, d, dtype=BF, device="cuda"), [T])
+
+
+def test_nan_codes_in_sight(cuda_lib):
+    """A key of NaN makes the outputs of its KV head NaN, a value element of NaN
+    its dim; the other heads and sequences keep their bits."""
+    hs2, d, page = cuda_lib, 64, 32
+    lengths = [900, 500]
+    pool = Pool(2, 3, d, page, 29, seed=23).fill(lengths, seed=24)
+    q = query(2, 12, d, 25)
+    o, lse = hs2.hs2_paged_decode(q, *pool.args(), ints(lengths))
+    pool.k[int(pool.table[0, 7]), 1, 3, 5] = 0x7F
+    pool.v[int(pool.table[1, 0]), 2, 9, 30] = 0xFF
+    o2, lse2 = hs2.hs2_paged_decode(q, *pool.args(), ints(lengths))
+    assert status(hs2) == 0
+    assert o2[0, 4:8].isnan().all() and lse2[0, 4:8].isnan().all()
+    assert o2[1, 8:, 30].isnan().all()
+    for x in (o, lse, o2, lse2):
+        x[0, 4:8] = 0
+    o[1, 8:, 30] = o2[1, 8:, 30] = 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
